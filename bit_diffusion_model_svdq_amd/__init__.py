@@ -52,7 +52,7 @@ EXPORTS = [
     "svdq_act_absmax_update_device", "svdq_forward_workspace_layout",
     "svdq_forward_workspace_layout_mxfp4", "svdq_static_workspace_bytes", "svdq_linear_forward_noalloc",
     "svdq_forward_fused", "svdq_debug_fused_forward", "svdq_forward_fused_mxfp4",
-    "svdq_debug_fused_forward_mxfp4",
+    "svdq_debug_fused_forward_mxfp4", "svdq_attention_workspace_bytes", "svdq_attention_forward",
 ]
 
 # svdq_activation
@@ -74,6 +74,7 @@ class svdq_pack_params(ctypes.Structure):
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_L = ctypes.c_int64
 _sig = {
     "svdq_act_absmax_update": [_P, ctypes.c_int64, _I, _P],
     "svdq_pack_weights": [_P, _I, _I, _P, ctypes.POINTER(svdq_pack_params), _P, _P, _P, _P, _P, _P],
@@ -106,6 +107,9 @@ _sig = {
     "svdq_forward_gemm_act_mxfp4": [_I, _I, _I, _I, _P, _P, _P, _P, _I, _P, _P, ctypes.c_size_t, _P],
     "svdq_mxfp4_tiled_scale_bytes": [_I, _I],
     "svdq_mxfp4_tile_scales": [_P, _I, _I, _P],
+    "svdq_attention_workspace_bytes": [_L, _L, _I, _I, _I, _I],
+    "svdq_attention_forward": [_P, _L, _P, _L, _P, _L, _P, _P, _I, _L, _L, _I, _I, _I, ctypes.c_float, _I, _P, _L,
+                               _P, _P, ctypes.c_size_t, _P],
     "svdq_status_string": [_I],
     "svdq_last_error": [],
 }
@@ -117,6 +121,7 @@ _lib.svdq_forward_workspace_bytes.restype = ctypes.c_size_t
 _lib.svdq_static_workspace_bytes.restype = ctypes.c_size_t
 _lib.svdq_forward_workspace_bytes_mxfp4.restype = ctypes.c_size_t
 _lib.svdq_mxfp4_tiled_scale_bytes.restype = ctypes.c_size_t
+_lib.svdq_attention_workspace_bytes.restype = ctypes.c_size_t
 _lib.svdq_status_string.restype = ctypes.c_char_p
 _lib.svdq_last_error.restype = ctypes.c_char_p
 
@@ -576,3 +581,76 @@ def svdq_quantize_activations_mxfp4(X, smooth, L1, qx, sx_e8m0, T, stream=None):
     st = _lib.svdq_quantize_activations_mxfp4(_dp(X), M, K, _dp(smooth), _dp(L1), r, _dp(qx),
                                               _dp(sx_e8m0), _dp(T), _stream(stream))
     _check(st, "svdq_quantize_activations_mxfp4")
+
+
+# ------------------------------------------------- the block around the linears
+def _launch(device, stream, call):
+    """call(stream) on the tensors' device: their own device's current stream unless one is given."""
+    import torch
+    if device.index is None or device.index == torch.cuda.current_device():
+        return call(_stream(stream))
+    with torch.cuda.device(device):
+        return call(_stream(stream))
+
+
+def _need_heads(t, name, head_dim=None, rows=None, heads=None):
+    """A [rows, heads, head_dim] bf16 tensor whose rows may lie apart (a column slice of a
+    projection's output); returns the row stride in elements."""
+    if not hasattr(t, "data_ptr") or not hasattr(t, "stride"):
+        raise TypeError(f"{name} must be a torch tensor on the GPU")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must live on the GPU (got device {t.device})")
+    dt = str(t.dtype).replace("torch.", "")
+    if dt not in _BF16:
+        raise ValueError(f"{name} must have dtype {' or '.join(_BF16)} (got {dt})")
+    if t.dim() != 3 or (rows, heads, head_dim) != tuple(
+            w if w is None else n for w, n in zip((rows, heads, head_dim), t.shape)):
+        raise ValueError(f"{name} must have shape {(rows, heads, head_dim)} (got {tuple(t.shape)})")
+    n, h, d = t.shape
+    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
+        raise ValueError(f"{name}: the heads of a row must be contiguous (strides {tuple(t.stride())})")
+    return t.stride(0) if n > 1 else h * d
+
+
+def _need_cu(cu, name, batch=None):
+    if cu is None:
+        return 1
+    _need(cu, name, ("int32",))
+    if cu.dim() != 1 or cu.numel() < 2 or (batch is not None and cu.numel() != batch + 1):
+        raise ValueError(f"{name} must hold batch + 1 offsets (got shape {tuple(cu.shape)})")
+    return cu.numel() - 1
+
+
+def _bytes(workspace):
+    return 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def svdq_attention_workspace_bytes(total_q: int, total_k: int, batch: int, heads_q: int, heads_kv: int,
+                                   head_dim: int) -> int:
+    return int(_lib.svdq_attention_workspace_bytes(total_q, total_k, batch, heads_q, heads_kv, head_dim))
+
+
+def svdq_attention_forward(Q, K, V, cu_q, cu_k, scale, causal, O, lse=None, workspace=None, stream=None):
+    """O [Tq, Hq, D] (written) = attention of Q [Tq, Hq, D] over K, V [Tk, Hkv, D], bf16, for packed
+    sequences with offsets cu_q, cu_k (int32 [batch + 1] on the GPU; None: one sequence).  Rows may lie
+    apart (slices of a fused projection's output).  lse: float32 [Hq, Tq] or None."""
+    ldq = _need_heads(Q, "Q")
+    total_q, heads_q, d = Q.shape
+    ldk = _need_heads(K, "K", d)
+    total_k, heads_kv = K.shape[:2]
+    ldv = _need_heads(V, "V", d, total_k, heads_kv)
+    ldo = _need_heads(O, "O", d, total_q, heads_q)
+    batch = _need_cu(cu_q, "cu_q")
+    if (cu_q is None) != (cu_k is None) and batch > 1:
+        raise ValueError("cu_q and cu_k must both be given for more than one sequence")
+    if cu_k is not None:
+        _need_cu(cu_k, "cu_k", batch)
+    _need(lse, "lse", ("float32",), (heads_q, total_q), optional=True)
+    if workspace is not None:
+        _need(workspace, "workspace", None)
+    _same_device(Q, K, V, O, cu_q, cu_k, lse, workspace)
+    st = _launch(Q.device, stream, lambda s: _lib.svdq_attention_forward(
+        _dp(Q), ldq, _dp(K), ldk, _dp(V), ldv, _dp(cu_q), _dp(cu_k), batch, total_q, total_k, heads_q, heads_kv, d,
+        scale, int(causal), _dp(O), ldo, _dp(lse), _dp(workspace), _bytes(workspace), s))
+    _check(st, "svdq_attention_forward")
+    return O

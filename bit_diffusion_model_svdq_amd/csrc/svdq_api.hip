@@ -1,5 +1,6 @@
 // C ABI entry points for the device side: argument validation, workspace
 // carving, kernel dispatch.  Host-side packing lives in pack.cpp.
+#include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
 #include <string.h>
@@ -263,6 +264,43 @@ svdq_status linear_forward_mx(const uint16_t* X, int M, int K, int N, int r, con
                    "mxfp4_gemm launch");
 }
 
+// ---- attention
+// Most workgroups of a launch: the runtime takes fewer than 2^32 work-items,
+// and no kernel here has more than 512 per workgroup.
+constexpr int64_t kMaxBlocks = (int64_t(1) << 23) - 1;
+
+svdq_status check_attention_shape(int batch, int64_t total_q, int64_t total_k, int heads_q, int heads_kv,
+                                  int head_dim) {
+  if (batch < 1) return fail(SVDQ_ERR_INVALID_ARG, "batch must be >= 1 (got %d)", batch);
+  if (total_q < 0 || total_k < 0)
+    return fail(SVDQ_ERR_INVALID_ARG, "negative total_q=%lld or total_k=%lld", (long long)total_q,
+                (long long)total_k);
+  if (heads_kv < 1 || heads_q < heads_kv || heads_q % heads_kv)
+    return fail(SVDQ_ERR_INVALID_ARG, "heads_q=%d must be a positive multiple of heads_kv=%d", heads_q, heads_kv);
+  if (head_dim < 8 || head_dim % 8)
+    return fail(SVDQ_ERR_INVALID_ARG, "head_dim must be a positive multiple of 8 (got %d)", head_dim);
+  if (head_dim > 128) return fail(SVDQ_ERR_UNSUPPORTED, "head_dim %d is above 128", head_dim);
+  if (total_q > INT32_MAX || total_k > INT32_MAX || total_q * (heads_q / heads_kv) > INT32_MAX - 512)
+    return fail(SVDQ_ERR_INVALID_ARG, "total_q=%lld (times %d heads a group) or total_k=%lld is beyond 31 bits",
+                (long long)total_q, heads_q / heads_kv, (long long)total_k);
+  if (total_q > 0 && attention_blocks((int)total_q, (int)total_k, batch, heads_q, heads_kv, head_dim) > kMaxBlocks)
+    return fail(SVDQ_ERR_INVALID_ARG, "too many rows for one launch: total_q=%lld, heads_q=%d, batch=%d",
+                (long long)total_q, heads_q, batch);
+  return SVDQ_OK;
+}
+
+svdq_status check_ld(int64_t ld, int64_t width, const char* name) {
+  if (ld < width || ld % 8)
+    return fail(SVDQ_ERR_INVALID_ARG, "%s=%lld must be a multiple of 8 and at least %lld", name, (long long)ld,
+                (long long)width);
+  return SVDQ_OK;
+}
+
+svdq_status check_align4(const void* p, const char* name) {
+  if (reinterpret_cast<uintptr_t>(p) & 3) return fail(SVDQ_ERR_ALIGNMENT, "%s is not 4-byte aligned", name);
+  return SVDQ_OK;
+}
+
 // ---- the allocation-free forward's workspace
 // A file-scope device array serves as the forward's workspace for callers
 // that cannot allocate.  Host code never uses the array's name as an address
@@ -457,6 +495,49 @@ svdq_status svdq_debug_group_partials(const uint8_t* qx, const uint8_t* Wq, int 
     return hip_check(
         launch_group_partials(qx, Wq, M, N, K, m0, m1, n0, n1, P, static_cast<hipStream_t>(stream)),
         "group_partials launch");
+  });
+}
+
+size_t svdq_attention_workspace_bytes(int64_t total_q, int64_t total_k, int batch, int heads_q, int heads_kv,
+                                      int head_dim) {
+  if (check_attention_shape(batch, total_q, total_k, heads_q, heads_kv, head_dim) != SVDQ_OK) return 0;
+  return attention_workspace((int)total_q, (int)total_k, batch, heads_q, heads_kv, head_dim);
+}
+
+svdq_status svdq_attention_forward(const uint16_t* Q, int64_t ldq, const uint16_t* K, int64_t ldk,
+                                   const uint16_t* V, int64_t ldv, const int32_t* cu_q, const int32_t* cu_k,
+                                   int batch, int64_t total_q, int64_t total_k, int heads_q, int heads_kv,
+                                   int head_dim, float scale, int causal, uint16_t* O, int64_t ldo, float* lse,
+                                   void* workspace, size_t workspace_bytes, void* stream) {
+  return guarded([&]() -> svdq_status {
+    SVDQ_TRY(check_attention_shape(batch, total_q, total_k, heads_q, heads_kv, head_dim));
+    if (!(scale > 0.f) || !isfinite(scale))
+      return fail(SVDQ_ERR_INVALID_ARG, "scale must be positive and finite (got %g)", (double)scale);
+    if (causal != 0 && causal != 1) return fail(SVDQ_ERR_INVALID_ARG, "causal must be 0 or 1 (got %d)", causal);
+    if (batch > 1 && (!cu_q || !cu_k))
+      return fail(SVDQ_ERR_INVALID_ARG, "cu_q and cu_k must not be NULL for batch=%d", batch);
+    const int64_t wq = (int64_t)heads_q * head_dim, wk = (int64_t)heads_kv * head_dim;
+    SVDQ_TRY(check_ld(ldq, wq, "ldq"));
+    SVDQ_TRY(check_ld(ldk, wk, "ldk"));
+    SVDQ_TRY(check_ld(ldv, wk, "ldv"));
+    SVDQ_TRY(check_ld(ldo, wq, "ldo"));
+    SVDQ_TRY(check_ptr(Q, "Q", total_q == 0));
+    SVDQ_TRY(check_ptr(K, "K", total_k == 0 || total_q == 0));
+    SVDQ_TRY(check_ptr(V, "V", total_k == 0 || total_q == 0));
+    SVDQ_TRY(check_ptr(O, "O", total_q == 0));
+    SVDQ_TRY(check_align4(cu_q, "cu_q"));
+    SVDQ_TRY(check_align4(cu_k, "cu_k"));
+    SVDQ_TRY(check_align4(lse, "lse"));
+    if (total_q == 0) return SVDQ_OK;
+    AttentionArgs a = {Q, K, V, ldq, ldk, ldv, ldo, cu_q, cu_k, batch, (int)total_q, (int)total_k, heads_q,
+                       heads_kv, head_dim, scale, causal, O, lse, workspace};
+    const size_t need = attention_workspace(a.total_q, a.total_k, batch, heads_q, heads_kv, head_dim);
+    if (need > 0) {
+      SVDQ_TRY(check_ptr(workspace, "workspace", false));
+      if (workspace_bytes < need)
+        return fail(SVDQ_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", need, workspace_bytes);
+    }
+    return hip_check(launch_attention(a, static_cast<hipStream_t>(stream)), "attention launch");
   });
 }
 

@@ -147,6 +147,25 @@ hipError_t launch_fused_smallk_mx(const FusedPlan& plan, const uint16_t* X, int 
                                   uint16_t* Y, int act, uint8_t* dbg_qx, uint8_t* dbg_sx,
                                   hipStream_t stream);
 
+// Attention over packed sequences (svdq_attention_forward).  cu_q / cu_k: row
+// offsets on the device, or NULL for one sequence of all rows.  workspace: the
+// bytes attention_workspace() gives (0: none needed).
+struct AttentionArgs {
+  const uint16_t *Q, *K, *V;
+  int64_t ldq, ldk, ldv, ldo;      // elements from one token's row to the next
+  const int32_t *cu_q, *cu_k;
+  int batch, total_q, total_k, heads_q, heads_kv, head_dim;
+  float scale;
+  int causal;
+  uint16_t* O;
+  float* lse;
+  void* workspace;
+};
+size_t attention_workspace(int total_q, int total_k, int batch, int heads_q, int heads_kv, int head_dim);
+// The largest grid of the call's launches, in workgroups of at most 512 threads.
+int64_t attention_blocks(int total_q, int total_k, int batch, int heads_q, int heads_kv, int head_dim);
+hipError_t launch_attention(const AttentionArgs& a, hipStream_t stream);
+
 // k2's main loop with the integer group partials exported instead of the epilogue.
 hipError_t launch_group_partials(const uint8_t* qx, const uint8_t* Wq, int M, int N, int K,
                                  int m0, int m1, int n0, int n1, int32_t* P, hipStream_t stream);

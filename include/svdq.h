@@ -361,6 +361,55 @@ svdq_status svdq_quantize_activations_mxfp4(const uint16_t* X, int M, int K, con
                                             const uint16_t* L1, int r, uint8_t* qx,
                                             uint8_t* sx_e8m0, float* T, void* stream);
 
+/* ------------------------------------------- the block around the linears
+ * What a transformer block of a 4-bit diffusion model runs between its
+ * SVDQuant linears: attention, the norms with their modulation, gate and
+ * residual, and the linears that stay in 16 bits.  All of them take device
+ * memory, run asynchronously on `stream` and allocate nothing.
+ *
+ * Packed sequences: `batch` sequences of different lengths lie behind each
+ * other in one tensor of rows.  cu [batch + 1] (int32, device memory) holds
+ * their offsets, ascending; sequence b is rows [cu[b], cu[b + 1]).  Rows before
+ * cu[0] and from cu[batch] on belong to no sequence: they are not read, and
+ * the outputs' rows there stay as they were.  A sequence may be empty.  cu
+ * may be NULL for batch = 1: one sequence of all rows.  The offsets are read
+ * by the kernels, never by the host; whatever they hold, no kernel accesses
+ * anything outside the tensors' rows (offsets that do not ascend give
+ * undefined results). */
+
+/* Workspace of svdq_attention_forward in bytes (partial rows where the keys of
+ * a tile are cut into shares; depends on the current device's compute-unit
+ * count).  0: none is needed, or the arguments are rejected. */
+size_t svdq_attention_workspace_bytes(int64_t total_q, int64_t total_k, int batch, int heads_q,
+                                      int heads_kv, int head_dim);
+
+/* Softmax attention of every query over the keys of its own sequence:
+ *   O[i, h] = sum_j softmax_j(scale Q[i, h] . K[j, h / G]) V[j, h / G],  G = heads_q / heads_kv
+ * bf16 in and out, products, softmax and sums in float32; the softmax's
+ * weights enter the product with V rounded to bf16 (the values' type).
+ *   Q [total_q, heads_q, head_dim], K, V [total_k, heads_kv, head_dim],
+ *   O [total_q, heads_q, head_dim]: rows ldq, ldk, ldv, ldo elements apart
+ *   (multiples of 8, so column slices of one projection's output serve as
+ *   they are); O must not overlap the inputs.
+ * Sequence b has query rows [cu_q[b], cu_q[b + 1]) and key rows
+ * [cu_k[b], cu_k[b + 1]); their numbers may differ (cross attention; new
+ * tokens against a longer history).  causal = 1: query i of nq sees the keys
+ * j <= i + nk - nq of nk, so that the last query sees the last key.
+ * A query that sees no key gets O = 0 and log-sum-exp -inf.
+ * lse (float32 [heads_q, total_q], may be NULL): ln sum_j exp(scale Q . K).
+ * Requires head_dim a multiple of 8 up to 128 (above: SVDQ_ERR_UNSUPPORTED),
+ * heads_q a multiple of heads_kv, scale positive and finite.  Non-finite K or
+ * V elements can reach every query of their sequence and key head, also the
+ * queries that the causal mask hides them from, but no other sequence.
+ * The sums run in an order that depends on the shapes only, so equal calls
+ * give equal bits. */
+svdq_status svdq_attention_forward(const uint16_t* Q, int64_t ldq, const uint16_t* K, int64_t ldk,
+                                   const uint16_t* V, int64_t ldv, const int32_t* cu_q,
+                                   const int32_t* cu_k, int batch, int64_t total_q, int64_t total_k,
+                                   int heads_q, int heads_kv, int head_dim, float scale, int causal,
+                                   uint16_t* O, int64_t ldo, float* lse, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
 const char* svdq_status_string(svdq_status status);
 const char* svdq_last_error(void);
 
