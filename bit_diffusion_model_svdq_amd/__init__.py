@@ -53,11 +53,17 @@ EXPORTS = [
     "svdq_forward_workspace_layout_mxfp4", "svdq_static_workspace_bytes", "svdq_linear_forward_noalloc",
     "svdq_forward_fused", "svdq_debug_fused_forward", "svdq_forward_fused_mxfp4",
     "svdq_debug_fused_forward_mxfp4", "svdq_attention_workspace_bytes", "svdq_attention_forward",
+    "svdq_block_norm_forward", "svdq_linear_bf16_workspace_bytes", "svdq_linear_bf16_forward",
 ]
 
 # svdq_activation
 SVDQ_ACT_NONE = 0
 SVDQ_ACT_GELU_TANH = 1
+SVDQ_ACT_SILU = 2               # svdq_linear_bf16_forward only
+
+# svdq_norm, svdq_dtype
+SVDQ_NORM_NONE, SVDQ_NORM_RMS, SVDQ_NORM_LAYER = 0, 1, 2
+SVDQ_BF16, SVDQ_F32 = 0, 1
 
 
 class SvdqError(RuntimeError):
@@ -110,6 +116,10 @@ _sig = {
     "svdq_attention_workspace_bytes": [_L, _L, _I, _I, _I, _I],
     "svdq_attention_forward": [_P, _L, _P, _L, _P, _L, _P, _P, _I, _L, _L, _I, _I, _I, ctypes.c_float, _I, _P, _L,
                                _P, _P, ctypes.c_size_t, _P],
+    "svdq_block_norm_forward": [_P, _I, _P, _L, _I, _P, _I, _I, _P, _P, _L, ctypes.c_float, ctypes.c_float, _I, _P, _P,
+                                _P, _L, _P, _L, ctypes.c_float, _P, _P, _P],
+    "svdq_linear_bf16_workspace_bytes": [_L, _I, _I],
+    "svdq_linear_bf16_forward": [_P, _L, _I, _I, _P, _P, _I, _P, _P, _I, _P, ctypes.c_size_t, _P],
     "svdq_status_string": [_I],
     "svdq_last_error": [],
 }
@@ -122,6 +132,7 @@ _lib.svdq_static_workspace_bytes.restype = ctypes.c_size_t
 _lib.svdq_forward_workspace_bytes_mxfp4.restype = ctypes.c_size_t
 _lib.svdq_mxfp4_tiled_scale_bytes.restype = ctypes.c_size_t
 _lib.svdq_attention_workspace_bytes.restype = ctypes.c_size_t
+_lib.svdq_linear_bf16_workspace_bytes.restype = ctypes.c_size_t
 _lib.svdq_status_string.restype = ctypes.c_char_p
 _lib.svdq_last_error.restype = ctypes.c_char_p
 
@@ -654,3 +665,76 @@ def svdq_attention_forward(Q, K, V, cu_q, cu_k, scale, causal, O, lse=None, work
         scale, int(causal), _dp(O), ldo, _dp(lse), _dp(workspace), _bytes(workspace), s))
     _check(st, "svdq_attention_forward")
     return O
+
+
+def _need_vectors(t, name, batch, width):
+    """Per-sequence bf16 vectors [batch, width] whose rows may lie apart; returns the row stride."""
+    if t is None:
+        return 0
+    if not hasattr(t, "data_ptr") or not hasattr(t, "stride"):
+        raise TypeError(f"{name} must be a torch tensor on the GPU")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must live on the GPU (got device {t.device})")
+    dt = str(t.dtype).replace("torch.", "")
+    if dt not in _BF16:
+        raise ValueError(f"{name} must have dtype {' or '.join(_BF16)} (got {dt})")
+    if tuple(t.shape) != (batch, width):
+        raise ValueError(f"{name} must have shape {(batch, width)} (got {tuple(t.shape)})")
+    if t.stride(1) != 1:
+        raise ValueError(f"{name}: the channels of a row must be contiguous (strides {tuple(t.stride())})")
+    return t.stride(0) if batch > 1 else width
+
+
+def svdq_block_norm_forward(x, y, cu, post, post_weight, gate, residual_scale, branch_scale, pre, pre_weight, pre_bias,
+                            scale, shift, eps, x_out, h, stream=None):
+    """x_out = residual_scale x + branch_scale gate post(y) post_weight and
+    h = (pre(x_out) pre_weight + pre_bias)(1 + scale) + shift, row by row ([rows, width]); post, pre:
+    SVDQ_NORM_*.  x and x_out float32 or bf16, everything else bf16; gate, scale, shift [batch, width]
+    (rows may lie apart).  cu: int32 [batch + 1] offsets of the packed sequences, None for one sequence.
+    Absent operands are None; x_out may be x and h may be y."""
+    if x.dim() != 2:
+        raise ValueError("x must be a [rows, width] tensor")
+    rows, width = x.shape
+    _need(x, "x", _BF16 + ("float32",))
+    f32 = str(x.dtype) == "torch.float32"
+    _need(x_out, "x_out", ("float32",) if f32 else _BF16, (rows, width), optional=True)
+    _need(y, "y", _BF16, (rows, width), optional=True)
+    _need(h, "h", _BF16, (rows, width), optional=True)
+    batch = _need_cu(cu, "cu")
+    for t, name in ((post_weight, "post_weight"), (pre_weight, "pre_weight"), (pre_bias, "pre_bias")):
+        _need(t, name, _BF16, (width,), optional=True)
+    ld = [_need_vectors(t, name, batch, width) for t, name in ((gate, "gate"), (scale, "scale"), (shift, "shift"))]
+    _same_device(x, y, cu, post_weight, gate, pre_weight, pre_bias, scale, shift, x_out, h)
+    st = _launch(x.device, stream, lambda s: _lib.svdq_block_norm_forward(
+        _dp(x), SVDQ_F32 if f32 else SVDQ_BF16, _dp(y), rows, width, _dp(cu), batch, post, _dp(post_weight), _dp(gate),
+        ld[0], residual_scale, branch_scale, pre, _dp(pre_weight), _dp(pre_bias), _dp(scale), ld[1], _dp(shift), ld[2],
+        eps, _dp(x_out), _dp(h), s))
+    _check(st, "svdq_block_norm_forward")
+    return x_out, h
+
+
+def svdq_linear_bf16_workspace_bytes(M: int, K: int, N: int) -> int:
+    return int(_lib.svdq_linear_bf16_workspace_bytes(M, K, N))
+
+
+def svdq_linear_bf16_forward(X, W, bias, activation, residual, Y, workspace=None, stream=None):
+    """Y [M, N] (written) = act(X W^T + bias) + residual; X [M, K], W [N, K], bias [N] bf16, Y and
+    residual bf16 or float32 alike (residual may be Y)."""
+    if X.dim() != 2 or W.dim() != 2:
+        raise ValueError("X must be a [M, K] and W a [N, K] tensor")
+    M, K = X.shape
+    N = W.shape[0]
+    _need(X, "X", _BF16)
+    _need(W, "W", _BF16, (N, K))
+    _need(bias, "bias", _BF16, (N,), optional=True)
+    _need(Y, "Y", _BF16 + ("float32",), (M, N))
+    f32 = str(Y.dtype) == "torch.float32"
+    _need(residual, "residual", ("float32",) if f32 else _BF16, (M, N), optional=True)
+    if workspace is not None:
+        _need(workspace, "workspace", None)
+    _same_device(X, W, bias, residual, Y, workspace)
+    st = _launch(X.device, stream, lambda s: _lib.svdq_linear_bf16_forward(
+        _dp(X), M, K, N, _dp(W), _dp(bias), int(activation), _dp(residual), _dp(Y), SVDQ_F32 if f32 else SVDQ_BF16,
+        _dp(workspace), _bytes(workspace), s))
+    _check(st, "svdq_linear_bf16_forward")
+    return Y

@@ -301,6 +301,30 @@ svdq_status check_align4(const void* p, const char* name) {
   return SVDQ_OK;
 }
 
+// ---- block norms and the 16-bit linear
+svdq_status check_dtype(int dtype, const char* name) {
+  if (dtype != SVDQ_BF16 && dtype != SVDQ_F32)
+    return fail(SVDQ_ERR_INVALID_ARG, "%s %d is not one of svdq_dtype", name, dtype);
+  return SVDQ_OK;
+}
+
+svdq_status check_norm(int kind, const char* name) {
+  if (kind != kNormNone && kind != kNormRms && kind != kNormLayer)
+    return fail(SVDQ_ERR_INVALID_ARG, "%s %d is not one of svdq_norm", name, kind);
+  return SVDQ_OK;
+}
+
+svdq_status check_linear_shape(int64_t M, int K, int N) {
+  if (M < 0 || M > INT32_MAX - 512)
+    return fail(SVDQ_ERR_INVALID_ARG, "M=%lld is negative or beyond 31 bits", (long long)M);
+  if (K < 8 || K % 8 || K > INT32_MAX - 512)
+    return fail(SVDQ_ERR_INVALID_ARG, "K must be a positive multiple of 8 (got %d)", K);
+  if (N < 1 || N > INT32_MAX - 512) return fail(SVDQ_ERR_INVALID_ARG, "N must be positive (got %d)", N);
+  if (M > 0 && linear_blocks((int)M, K, N) > kMaxBlocks)
+    return fail(SVDQ_ERR_INVALID_ARG, "M=%lld x N=%d is too much for one launch", (long long)M, N);
+  return SVDQ_OK;
+}
+
 // ---- the allocation-free forward's workspace
 // A file-scope device array serves as the forward's workspace for callers
 // that cannot allocate.  Host code never uses the array's name as an address
@@ -538,6 +562,87 @@ svdq_status svdq_attention_forward(const uint16_t* Q, int64_t ldq, const uint16_
         return fail(SVDQ_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", need, workspace_bytes);
     }
     return hip_check(launch_attention(a, static_cast<hipStream_t>(stream)), "attention launch");
+  });
+}
+
+svdq_status svdq_block_norm_forward(const void* x, int stream_dtype, const uint16_t* y, int64_t rows, int width,
+                                    const int32_t* cu, int batch, int post, const uint16_t* post_weight,
+                                    const uint16_t* gate, int64_t ld_gate, float residual_scale,
+                                    float branch_scale, int pre, const uint16_t* pre_weight,
+                                    const uint16_t* pre_bias, const uint16_t* scale, int64_t ld_scale,
+                                    const uint16_t* shift, int64_t ld_shift, float eps, void* x_out, uint16_t* h,
+                                    void* stream) {
+  return guarded([&]() -> svdq_status {
+    if (rows < 0 || rows > kMaxBlocks)
+      return fail(SVDQ_ERR_INVALID_ARG, "rows=%lld is negative or above %lld", (long long)rows,
+                  (long long)kMaxBlocks);
+    if (width < 8 || width % 8 || width > kMaxNormWidth)
+      return fail(SVDQ_ERR_INVALID_ARG, "width must be a multiple of 8 in [8, %d] (got %d)", kMaxNormWidth, width);
+    if (batch < 1) return fail(SVDQ_ERR_INVALID_ARG, "batch must be >= 1 (got %d)", batch);
+    if (batch > 1 && !cu) return fail(SVDQ_ERR_INVALID_ARG, "cu must not be NULL for batch=%d", batch);
+    SVDQ_TRY(check_dtype(stream_dtype, "stream_dtype"));
+    SVDQ_TRY(check_norm(post, "post"));
+    SVDQ_TRY(check_norm(pre, "pre"));
+    if (!y && (post != kNormNone || post_weight || gate))
+      return fail(SVDQ_ERR_INVALID_ARG, "post norm, its weight or a gate without y");
+    if (!h && (pre != kNormNone || pre_weight || pre_bias || scale || shift))
+      return fail(SVDQ_ERR_INVALID_ARG, "pre norm, its weights or a modulation without h");
+    if (!x_out && !h) return fail(SVDQ_ERR_INVALID_ARG, "x_out and h are both NULL");
+    if (!(eps >= 0.f) || !isfinite(eps))
+      return fail(SVDQ_ERR_INVALID_ARG, "eps must be finite and not negative (got %g)", (double)eps);
+    if (!isfinite(residual_scale) || !isfinite(branch_scale))
+      return fail(SVDQ_ERR_INVALID_ARG, "residual_scale and branch_scale must be finite");
+    if (gate) SVDQ_TRY(check_ld(ld_gate, width, "ld_gate"));
+    if (scale) SVDQ_TRY(check_ld(ld_scale, width, "ld_scale"));
+    if (shift) SVDQ_TRY(check_ld(ld_shift, width, "ld_shift"));
+    SVDQ_TRY(check_ptr(x, "x", rows == 0));
+    SVDQ_TRY(check_ptr(y, "y", true));
+    SVDQ_TRY(check_ptr(post_weight, "post_weight", true));
+    SVDQ_TRY(check_ptr(gate, "gate", true));
+    SVDQ_TRY(check_ptr(pre_weight, "pre_weight", true));
+    SVDQ_TRY(check_ptr(pre_bias, "pre_bias", true));
+    SVDQ_TRY(check_ptr(scale, "scale", true));
+    SVDQ_TRY(check_ptr(shift, "shift", true));
+    SVDQ_TRY(check_ptr(x_out, "x_out", true));
+    SVDQ_TRY(check_ptr(h, "h", true));
+    SVDQ_TRY(check_align4(cu, "cu"));
+    if (rows == 0) return SVDQ_OK;
+    const BlockNormArgs a = {x, y, rows, width, cu, batch, post, post_weight, gate, ld_gate, residual_scale,
+                             branch_scale, pre, pre_weight, pre_bias, scale, ld_scale, shift, ld_shift, eps, x_out,
+                             h};
+    return hip_check(launch_block_norm(a, stream_dtype == SVDQ_F32, static_cast<hipStream_t>(stream)),
+                     "block_norm launch");
+  });
+}
+
+size_t svdq_linear_bf16_workspace_bytes(int64_t M, int K, int N) {
+  if (check_linear_shape(M, K, N) != SVDQ_OK || M == 0) return 0;
+  return linear_workspace((int)M, K, N);
+}
+
+svdq_status svdq_linear_bf16_forward(const uint16_t* X, int64_t M, int K, int N, const uint16_t* W,
+                                     const uint16_t* bias, int activation, const void* residual, void* Y,
+                                     int out_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  return guarded([&]() -> svdq_status {
+    SVDQ_TRY(check_linear_shape(M, K, N));
+    SVDQ_TRY(check_dtype(out_dtype, "out_dtype"));
+    if (activation != kActNone && activation != kActGeluTanh && activation != kActSilu)
+      return fail(SVDQ_ERR_INVALID_ARG, "activation %d is not one of svdq_activation", activation);
+    SVDQ_TRY(check_ptr(X, "X", M == 0));
+    SVDQ_TRY(check_ptr(W, "W", M == 0));
+    SVDQ_TRY(check_ptr(bias, "bias", true));
+    SVDQ_TRY(check_ptr(residual, "residual", true));
+    SVDQ_TRY(check_ptr(Y, "Y", M == 0));
+    if (M == 0) return SVDQ_OK;
+    const size_t need = linear_workspace((int)M, K, N);
+    if (need > 0) {
+      SVDQ_TRY(check_ptr(workspace, "workspace", false));
+      if (workspace_bytes < need)
+        return fail(SVDQ_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", need, workspace_bytes);
+    }
+    LinearArgs a = {X, W, bias, residual, Y, (int)M, K, N, static_cast<float*>(workspace), 1, 0, false};
+    return hip_check(launch_linear_bf16(a, activation, out_dtype == SVDQ_F32, static_cast<hipStream_t>(stream)),
+                     "linear_bf16 launch");
   });
 }
 

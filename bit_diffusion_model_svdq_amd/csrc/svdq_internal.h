@@ -98,6 +98,7 @@ __device__ inline void lds_barrier() {
 // Output activations of the GEMM epilogue (the values of svdq_activation).
 constexpr int kActNone = 0;
 constexpr int kActGeluTanh = 1;
+constexpr int kActSilu = 2;      // the 16-bit linear only
 
 // k2: Y = act(sum_g sx sw P_g + T L2^T + b), bf16 out.  T holds t_slices
 // partial sums of M x r floats, added in order.
@@ -165,6 +166,50 @@ size_t attention_workspace(int total_q, int total_k, int batch, int heads_q, int
 // The largest grid of the call's launches, in workgroups of at most 512 threads.
 int64_t attention_blocks(int total_q, int total_k, int batch, int heads_q, int heads_kv, int head_dim);
 hipError_t launch_attention(const AttentionArgs& a, hipStream_t stream);
+
+// Norms (the values of svdq_norm) and svdq_block_norm_forward's operands; NULL
+// where absent, row strides of the per-sequence vectors in elements.
+constexpr int kNormNone = 0;
+constexpr int kNormRms = 1;
+constexpr int kNormLayer = 2;
+constexpr int kMaxNormWidth = 16384;
+struct BlockNormArgs {
+  const void* x;
+  const uint16_t* y;
+  int64_t rows;
+  int width;
+  const int32_t* cu;
+  int batch;
+  int post;
+  const uint16_t* post_weight;
+  const uint16_t* gate;
+  int64_t ld_gate;
+  float residual_scale, branch_scale;
+  int pre;
+  const uint16_t *pre_weight, *pre_bias;
+  const uint16_t* scale;
+  int64_t ld_scale;
+  const uint16_t* shift;
+  int64_t ld_shift;
+  float eps;
+  void* x_out;
+  uint16_t* h;
+};
+// fp32: the type of x and x_out (else bf16).
+hipError_t launch_block_norm(const BlockNormArgs& a, bool fp32, hipStream_t stream);
+
+// The 16-bit linear Y = act(X W^T + bias) + residual; Y and the residual float32
+// (fp32) or bf16.  The caller fills the first line and part (the workspace,
+// linear_workspace() bytes).
+struct LinearArgs {
+  const uint16_t *X, *W, *bias; const void* residual; void* Y; int M, K, N;
+  float* part;
+  int splits, part_ld;
+  bool wide;               // rows of Y are aligned for four outputs at once
+};
+size_t linear_workspace(int M, int K, int N);
+int64_t linear_blocks(int M, int K, int N);
+hipError_t launch_linear_bf16(LinearArgs a, int act, bool fp32, hipStream_t stream);
 
 // k2's main loop with the integer group partials exported instead of the epilogue.
 hipError_t launch_group_partials(const uint8_t* qx, const uint8_t* Wq, int M, int N, int K,

@@ -162,11 +162,13 @@ svdq_status svdq_linear_forward(const uint16_t* X, int M, int K, int N, int r,
  * "Gaussian Error Linear Units", section 2),
  *   0.5 y (1 + tanh(sqrt(2/pi) (y + 0.044715 y^3))),
  * the activation between the up and down projections of a DiT MLP; fusing it
- * here lets the up projection's output feed the down projection directly. */
-typedef enum { SVDQ_ACT_NONE = 0, SVDQ_ACT_GELU_TANH = 1 } svdq_activation;
+ * here lets the up projection's output feed the down projection directly.
+ * SVDQ_ACT_SILU, y / (1 + e^-y), is for svdq_linear_bf16_forward only: the
+ * SVDQuant forwards do not implement it. */
+typedef enum { SVDQ_ACT_NONE = 0, SVDQ_ACT_GELU_TANH = 1, SVDQ_ACT_SILU = 2 } svdq_activation;
 
-/* svdq_linear_forward with `activation` (an svdq_activation value; any other
- * value is SVDQ_ERR_INVALID_ARG) applied to Y. */
+/* svdq_linear_forward with `activation` (SVDQ_ACT_NONE or SVDQ_ACT_GELU_TANH; any
+ * other value is SVDQ_ERR_INVALID_ARG) applied to Y. */
 svdq_status svdq_linear_forward_act(const uint16_t* X, int M, int K, int N, int r,
                                     const float* smooth, const uint16_t* L1, const uint16_t* L2,
                                     const uint8_t* Wq, const float* w_scales,
@@ -409,6 +411,53 @@ svdq_status svdq_attention_forward(const uint16_t* Q, int64_t ldq, const uint16_
                                    int heads_q, int heads_kv, int head_dim, float scale, int causal,
                                    uint16_t* O, int64_t ldo, float* lse, void* workspace,
                                    size_t workspace_bytes, void* stream);
+
+/* Types of a residual stream and of svdq_linear_bf16_forward's output. */
+typedef enum { SVDQ_BF16 = 0, SVDQ_F32 = 1 } svdq_dtype;
+
+/* Norms over a row of `width` channels, with statistics in float32 (the squares
+ * must not overflow it): v / sqrt(mean v^2 + eps), and
+ * (v - mean v) / sqrt(mean (v - mean v)^2 + eps). */
+typedef enum { SVDQ_NORM_NONE = 0, SVDQ_NORM_RMS = 1, SVDQ_NORM_LAYER = 2 } svdq_norm;
+
+/* What stands between two linears of a block: the norm after the branch that
+ * ends, its gate and the residual sum, then the norm before the branch that
+ * begins and its modulation.  For every row m of sequence b:
+ *   x_out[m] = residual_scale x[m] + branch_scale gate[b] post(y[m]) post_weight
+ *   h[m]     = (pre(x_out[m]) pre_weight + pre_bias) (1 + scale[b]) + shift[b]
+ * in float32, h from the unrounded x_out.  x, x_out [rows, width] have type
+ * `stream_dtype` (an svdq_dtype); y, h [rows, width] and all vectors are bf16.
+ * gate, scale, shift: one row per sequence, ld_* elements apart (column slices
+ * of the modulation linear's output; each a multiple of 8).  Any vector may be
+ * NULL (weights and gate 1, the others 0); y may be NULL (no branch: post must
+ * then be SVDQ_NORM_NONE, post_weight and gate NULL), and so may x_out, or h
+ * with everything that makes it.  x_out may be x, and h may be y; otherwise
+ * outputs must not overlap inputs.  width: a multiple of 8 up to 16384.
+ * Packed sequences as above (cu, batch). */
+svdq_status svdq_block_norm_forward(const void* x, int stream_dtype, const uint16_t* y, int64_t rows,
+                                    int width, const int32_t* cu, int batch, int post,
+                                    const uint16_t* post_weight, const uint16_t* gate,
+                                    int64_t ld_gate, float residual_scale, float branch_scale,
+                                    int pre, const uint16_t* pre_weight, const uint16_t* pre_bias,
+                                    const uint16_t* scale, int64_t ld_scale, const uint16_t* shift,
+                                    int64_t ld_shift, float eps, void* x_out, uint16_t* h,
+                                    void* stream);
+
+/* Workspace of svdq_linear_bf16_forward in bytes (float32 sums where the
+ * channels are cut into shares; depends on the current device's compute-unit
+ * count).  0: none is needed, or the shape is rejected. */
+size_t svdq_linear_bf16_workspace_bytes(int64_t M, int K, int N);
+
+/* The linear of a layer that stays in 16 bits (embeddings, modulation, final
+ * projection): Y = act(X W^T + bias) + residual, X [M, K], W [N, K], bias [N]
+ * bf16, sums in float32, one rounding.  Y and residual [M, N] have type
+ * `out_dtype` (an svdq_dtype); bias and residual may be NULL, and residual may
+ * be Y.  `activation` is any svdq_activation.  K a multiple of 8; any M >= 0
+ * (M = 0 does nothing) and N >= 1. */
+svdq_status svdq_linear_bf16_forward(const uint16_t* X, int64_t M, int K, int N, const uint16_t* W,
+                                     const uint16_t* bias, int activation, const void* residual,
+                                     void* Y, int out_dtype, void* workspace,
+                                     size_t workspace_bytes, void* stream);
 
 const char* svdq_status_string(svdq_status status);
 const char* svdq_last_error(void);
