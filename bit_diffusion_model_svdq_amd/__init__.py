@@ -231,6 +231,16 @@ def _dp(t):
 _BF16 = ("int16", "bfloat16")      # bf16 bit patterns: int16 views or torch.bfloat16
 
 
+_DTYPE_NAMES = {}                  # torch dtype -> its name without "torch."
+
+
+def _dtype_name(t):
+    n = _DTYPE_NAMES.get(t.dtype)
+    if n is None:
+        n = _DTYPE_NAMES[t.dtype] = str(t.dtype).replace("torch.", "")
+    return n
+
+
 def _need(t, name, dtypes, shape=None, numel=None, optional=False):
     if t is None:
         if optional:
@@ -242,16 +252,25 @@ def _need(t, name, dtypes, shape=None, numel=None, optional=False):
         raise ValueError(f"{name} must live on the GPU (got device {t.device})")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    dt = str(t.dtype).replace("torch.", "")
-    if dtypes is not None and dt not in dtypes:
-        raise ValueError(f"{name} must have dtype {' or '.join(dtypes)} (got {dt})")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if dtypes is not None and _dtype_name(t) not in dtypes:
+        raise ValueError(f"{name} must have dtype {' or '.join(dtypes)} (got {_dtype_name(t)})")
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
     if numel is not None and t.numel() != numel:
         raise ValueError(f"{name} must hold {numel} elements (got {t.numel()})")
 
 
 def _same_device(*ts):
+    first = None
+    for t in ts:
+        if t is None:
+            continue
+        if first is None:
+            first = t.device
+        elif t.device != first:
+            break
+    else:
+        return
     devs = {t.device for t in ts if t is not None}
     if len(devs) > 1:
         raise ValueError(f"tensors live on different devices: {sorted(str(d) for d in devs)}")
@@ -595,13 +614,33 @@ def svdq_quantize_activations_mxfp4(X, smooth, L1, qx, sx_e8m0, T, stream=None):
 
 
 # ------------------------------------------------- the block around the linears
-def _launch(device, stream, call):
-    """call(stream) on the tensors' device: their own device's current stream unless one is given."""
-    import torch
-    if device.index is None or device.index == torch.cuda.current_device():
-        return call(_stream(stream))
-    with torch.cuda.device(device):
-        return call(_stream(stream))
+_BF16_F32 = _BF16 + ("float32",)
+
+
+def _launch(device, stream, name, *args):
+    """The library's function on the tensors' device, with its current stream unless one is given."""
+    index = device.index
+    if index is not None and index != _torch.cuda.current_device():
+        with _torch.cuda.device(device):
+            return _launch(device, stream, name, *args)
+    s = _current_stream(index) if stream is None else stream.cuda_stream
+    st = getattr(_lib, name)(*args, s)
+    if st != SVDQ_OK:
+        raise SvdqError(st, name)
+
+
+# the raw handle of the current stream; building torch's Stream object takes longer than a launch
+_raw_stream = getattr(getattr(_torch, "_C", None), "_cuda_getCurrentRawStream", None)
+
+
+def _current_stream(index):
+    if _raw_stream is not None and index is not None:
+        return _raw_stream(index)
+    return _torch.cuda.current_stream().cuda_stream
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _need_heads(t, name, head_dim=None, rows=None, heads=None):
@@ -611,16 +650,17 @@ def _need_heads(t, name, head_dim=None, rows=None, heads=None):
         raise TypeError(f"{name} must be a torch tensor on the GPU")
     if t.device.type != "cuda":
         raise ValueError(f"{name} must live on the GPU (got device {t.device})")
-    dt = str(t.dtype).replace("torch.", "")
-    if dt not in _BF16:
-        raise ValueError(f"{name} must have dtype {' or '.join(_BF16)} (got {dt})")
-    if t.dim() != 3 or (rows, heads, head_dim) != tuple(
-            w if w is None else n for w, n in zip((rows, heads, head_dim), t.shape)):
-        raise ValueError(f"{name} must have shape {(rows, heads, head_dim)} (got {tuple(t.shape)})")
-    n, h, d = t.shape
-    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
-        raise ValueError(f"{name}: the heads of a row must be contiguous (strides {tuple(t.stride())})")
-    return t.stride(0) if n > 1 else h * d
+    if _dtype_name(t) not in _BF16:
+        raise ValueError(f"{name} must have dtype {' or '.join(_BF16)} (got {_dtype_name(t)})")
+    shape = t.shape
+    if (len(shape) != 3 or (rows is not None and shape[0] != rows) or (heads is not None and shape[1] != heads)
+            or (head_dim is not None and shape[2] != head_dim)):
+        raise ValueError(f"{name} must have shape {(rows, heads, head_dim)} (got {tuple(shape)})")
+    n, h, d = shape
+    ld, between, inner = t.stride()
+    if (d > 1 and inner != 1) or (h > 1 and between != d):
+        raise ValueError(f"{name}: the heads of a row must be contiguous (strides {(ld, between, inner)})")
+    return ld if n > 1 else h * d
 
 
 def _need_cu(cu, name, batch=None):
@@ -660,10 +700,9 @@ def svdq_attention_forward(Q, K, V, cu_q, cu_k, scale, causal, O, lse=None, work
     if workspace is not None:
         _need(workspace, "workspace", None)
     _same_device(Q, K, V, O, cu_q, cu_k, lse, workspace)
-    st = _launch(Q.device, stream, lambda s: _lib.svdq_attention_forward(
-        _dp(Q), ldq, _dp(K), ldk, _dp(V), ldv, _dp(cu_q), _dp(cu_k), batch, total_q, total_k, heads_q, heads_kv, d,
-        scale, int(causal), _dp(O), ldo, _dp(lse), _dp(workspace), _bytes(workspace), s))
-    _check(st, "svdq_attention_forward")
+    _launch(Q.device, stream, "svdq_attention_forward", _ptr(Q), ldq, _ptr(K), ldk, _ptr(V), ldv, _ptr(cu_q), _ptr(cu_k),
+            batch, total_q, total_k, heads_q, heads_kv, d, scale, int(causal), _ptr(O), ldo, _ptr(lse), _ptr(workspace),
+            _bytes(workspace))
     return O
 
 
@@ -675,10 +714,9 @@ def _need_vectors(t, name, batch, width):
         raise TypeError(f"{name} must be a torch tensor on the GPU")
     if t.device.type != "cuda":
         raise ValueError(f"{name} must live on the GPU (got device {t.device})")
-    dt = str(t.dtype).replace("torch.", "")
-    if dt not in _BF16:
-        raise ValueError(f"{name} must have dtype {' or '.join(_BF16)} (got {dt})")
-    if tuple(t.shape) != (batch, width):
+    if _dtype_name(t) not in _BF16:
+        raise ValueError(f"{name} must have dtype {' or '.join(_BF16)} (got {_dtype_name(t)})")
+    if t.shape != (batch, width):
         raise ValueError(f"{name} must have shape {(batch, width)} (got {tuple(t.shape)})")
     if t.stride(1) != 1:
         raise ValueError(f"{name}: the channels of a row must be contiguous (strides {tuple(t.stride())})")
@@ -695,8 +733,8 @@ def svdq_block_norm_forward(x, y, cu, post, post_weight, gate, residual_scale, b
     if x.dim() != 2:
         raise ValueError("x must be a [rows, width] tensor")
     rows, width = x.shape
-    _need(x, "x", _BF16 + ("float32",))
-    f32 = str(x.dtype) == "torch.float32"
+    _need(x, "x", _BF16_F32)
+    f32 = _dtype_name(x) == "float32"
     _need(x_out, "x_out", ("float32",) if f32 else _BF16, (rows, width), optional=True)
     _need(y, "y", _BF16, (rows, width), optional=True)
     _need(h, "h", _BF16, (rows, width), optional=True)
@@ -705,11 +743,9 @@ def svdq_block_norm_forward(x, y, cu, post, post_weight, gate, residual_scale, b
         _need(t, name, _BF16, (width,), optional=True)
     ld = [_need_vectors(t, name, batch, width) for t, name in ((gate, "gate"), (scale, "scale"), (shift, "shift"))]
     _same_device(x, y, cu, post_weight, gate, pre_weight, pre_bias, scale, shift, x_out, h)
-    st = _launch(x.device, stream, lambda s: _lib.svdq_block_norm_forward(
-        _dp(x), SVDQ_F32 if f32 else SVDQ_BF16, _dp(y), rows, width, _dp(cu), batch, post, _dp(post_weight), _dp(gate),
-        ld[0], residual_scale, branch_scale, pre, _dp(pre_weight), _dp(pre_bias), _dp(scale), ld[1], _dp(shift), ld[2],
-        eps, _dp(x_out), _dp(h), s))
-    _check(st, "svdq_block_norm_forward")
+    _launch(x.device, stream, "svdq_block_norm_forward", _ptr(x), SVDQ_F32 if f32 else SVDQ_BF16, _ptr(y), rows, width,
+            _ptr(cu), batch, post, _ptr(post_weight), _ptr(gate), ld[0], residual_scale, branch_scale, pre,
+            _ptr(pre_weight), _ptr(pre_bias), _ptr(scale), ld[1], _ptr(shift), ld[2], eps, _ptr(x_out), _ptr(h))
     return x_out, h
 
 
@@ -727,14 +763,12 @@ def svdq_linear_bf16_forward(X, W, bias, activation, residual, Y, workspace=None
     _need(X, "X", _BF16)
     _need(W, "W", _BF16, (N, K))
     _need(bias, "bias", _BF16, (N,), optional=True)
-    _need(Y, "Y", _BF16 + ("float32",), (M, N))
-    f32 = str(Y.dtype) == "torch.float32"
+    _need(Y, "Y", _BF16_F32, (M, N))
+    f32 = _dtype_name(Y) == "float32"
     _need(residual, "residual", ("float32",) if f32 else _BF16, (M, N), optional=True)
     if workspace is not None:
         _need(workspace, "workspace", None)
     _same_device(X, W, bias, residual, Y, workspace)
-    st = _launch(X.device, stream, lambda s: _lib.svdq_linear_bf16_forward(
-        _dp(X), M, K, N, _dp(W), _dp(bias), int(activation), _dp(residual), _dp(Y), SVDQ_F32 if f32 else SVDQ_BF16,
-        _dp(workspace), _bytes(workspace), s))
-    _check(st, "svdq_linear_bf16_forward")
+    _launch(X.device, stream, "svdq_linear_bf16_forward", _ptr(X), M, K, N, _ptr(W), _ptr(bias), int(activation),
+            _ptr(residual), _ptr(Y), SVDQ_F32 if f32 else SVDQ_BF16, _ptr(workspace), _bytes(workspace))
     return Y
