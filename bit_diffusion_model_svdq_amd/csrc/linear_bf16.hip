@@ -6,16 +6,28 @@
 // accumulators, one rounding to the output's type.  The residual enters as
 // Y's type.
 //
-// Two kernels.  linear_tile: a workgroup computes a BM x BN tile of Y on the
-// 16x16x32 bf16 MFMA from a ring of NR LDS buffers, one step of 32 channels
-// each, filled by direct copies (global_load_lds) NR - 1 steps ahead; where
-// the tiles do not fill the chip the channels are cut into shares whose
-// float32 sums linear_join brings together.  linear_rows: few rows of X;
-// then the weight's bytes are the cost, and each wave streams its share of the
-// channels of a few weight rows straight into registers.
+// Three kernels, all on the 16x16x32 bf16 MFMA with Y^T tiles (W rows as the
+// MFMA's A operand, X rows as B): a lane's four accumulators are then
+// neighbouring outputs of one row of Y.  A step is 64 channels: a row's step
+// is one 128-byte line, moved whole by direct copies into LDS
+// (global_load_lds).  With steps of 32 channels the half lines cost twice the
+// requests: the L2 then delivers 16 TB/s instead of 28.
 //
-// Both compute Y^T tiles (W rows as the MFMA's A operand, X rows as B): a
-// lane's four accumulators are then neighbouring outputs of one row of Y.
+//   linear_tile   a ring of NR LDS buffers, NR - 1 steps of copies in flight,
+//                 one barrier a step; 128 x 128, 128 x 64 and 64 x 64 tiles.
+//                 Where tiles are few, the channels are cut into shares whose
+//                 float32 sums linear_join brings together.
+//   linear_turns  256 x 256, eight waves in two groups that take turns: while
+//                 one group's MFMAs run, the other reads its fragments.  Large
+//                 products: the tile moves the fewest bytes per operation.
+//   linear_rows   up to 16 rows of X: the weight's bytes are the cost, and each
+//                 wave streams its share of the channels of 16 weight rows
+//                 straight into registers.
+//
+// Measured: 4608 x 3072 -> 12288 330 us (1053 TFLOP/s) with 256 x 256 turns, 347
+// with the same tile in one group, 357 / 442 / 501 with the smaller tiles;
+// 1155 x 1288 -> 1290 16.2 us with 128 x 64, 16.8 with 64 x 64, 27 with 128 x 128;
+// 2 x 3072 -> 18432 23.7 us (4.8 TB/s) in linear_rows.
 #include <algorithm>
 
 #include "gemm_tail.h"
@@ -29,9 +41,6 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) void* lds_ptr;
-
-constexpr int KS = 32;            // channels per step: one MFMA deep
-constexpr int ROWB = KS * 2;      // bytes of a row's step
 
 __device__ inline float bf16_value(uint16_t b) { return __uint_as_float(uint32_t(b) << 16); }
 
@@ -47,57 +56,65 @@ __device__ inline float activate(float v) {
   return v;
 }
 
+// Vectors of four at any element's alignment: rows of Y need not start on a
+// 16-byte boundary, and the memory pipeline takes such accesses whole.
+typedef f32x4 f32x4u __attribute__((aligned(4)));
+typedef u32x2 u32x2u __attribute__((aligned(2)));
+
+__device__ inline f32x4 unpack4(u32x2 b) {
+  return f32x4{__uint_as_float(b[0] << 16), __uint_as_float(b[0] & 0xFFFF0000u), __uint_as_float(b[1] << 16),
+               __uint_as_float(b[1] & 0xFFFF0000u)};
+}
+
+// bias[n .. n + 3], zeros past the row and where there is none
+__device__ inline f32x4 bias4(const LinearArgs& a, int n) {
+  f32x4 v = f32x4{0.f, 0.f, 0.f, 0.f};
+  if (!a.bias || n >= a.N) return v;
+  if (n + 4 <= a.N) return unpack4(*reinterpret_cast<const u32x2u*>(a.bias + n));
+  for (int i = 0; i < 4; ++i)
+    if (n + i < a.N) v[i] = bf16_value(a.bias[n + i]);
+  return v;
+}
+
 // Four neighbouring outputs n .. n + 3 of row m: bias, activation, residual,
-// rounding, store.  `wide`: N is a multiple of 4 and the base pointers are
-// 16-byte aligned, so the four are stored (and the residual read) at once.
+// rounding, store.
 template <class O, int ACT>
-__device__ inline void finish4(f32x4 v, const LinearArgs& a, int64_t m, int n, bool wide) {
+__device__ inline void finish4(f32x4 v, f32x4 bias, const LinearArgs& a, int64_t m, int n) {
   if (m >= a.M || n >= a.N) return;
   const int64_t at = m * a.N + n;
   O* y = static_cast<O*>(a.Y) + at;
   const O* r = a.residual ? static_cast<const O*>(a.residual) + at : nullptr;
-  if (wide) {
-    if (a.bias) {
-      const u32x2 b = *reinterpret_cast<const u32x2*>(a.bias + n);
-      v[0] += __uint_as_float(b[0] << 16);
-      v[1] += __uint_as_float(b[0] & 0xFFFF0000u);
-      v[2] += __uint_as_float(b[1] << 16);
-      v[3] += __uint_as_float(b[1] & 0xFFFF0000u);
-    }
+  v += bias;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = activate<ACT>(v[i]);
+  for (int i = 0; i < 4; ++i) v[i] = activate<ACT>(v[i]);
+  if (n + 4 <= a.N) {
     if constexpr (sizeof(O) == 4) {
-      if (r) v += *reinterpret_cast<const f32x4*>(r);
-      *reinterpret_cast<f32x4*>(y) = v;
+      if (r) v += *reinterpret_cast<const f32x4u*>(r);
+      *reinterpret_cast<f32x4u*>(y) = v;
     } else {
-      if (r) {
-        const u32x2 b = *reinterpret_cast<const u32x2*>(r);
-        v[0] += __uint_as_float(b[0] << 16);
-        v[1] += __uint_as_float(b[0] & 0xFFFF0000u);
-        v[2] += __uint_as_float(b[1] << 16);
-        v[3] += __uint_as_float(b[1] & 0xFFFF0000u);
-      }
+      if (r) v += unpack4(*reinterpret_cast<const u32x2u*>(r));
       u32x2 w;
 #pragma unroll
       for (int i = 0; i < 2; ++i)
         w[i] = __builtin_bit_cast(uint16_t, (__bf16)v[2 * i]) |
                ((uint32_t)__builtin_bit_cast(uint16_t, (__bf16)v[2 * i + 1]) << 16);
-      *reinterpret_cast<u32x2*>(y) = w;
+      *reinterpret_cast<u32x2u*>(y) = w;
     }
     return;
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if (n + i >= a.N) break;
-    float u = activate<ACT>(v[i] + (a.bias ? bf16_value(a.bias[n + i]) : 0.f));
-    if constexpr (sizeof(O) == 4) {
-      y[i] = r ? u + r[i] : u;
-    } else {
-      if (r) u += bf16_value(r[i]);
-      y[i] = __builtin_bit_cast(uint16_t, (__bf16)u);
-    }
+    if constexpr (sizeof(O) == 4)
+      y[i] = r ? v[i] + r[i] : v[i];
+    else
+      y[i] = __builtin_bit_cast(uint16_t, (__bf16)(r ? v[i] + bf16_value(r[i]) : v[i]));
   }
 }
+
+constexpr int KS = 64;            // channels per step: two MFMAs deep
+constexpr int ROWB = KS * 2;      // bytes of a row's step, one line
+constexpr int CHUNKS = ROWB / 16;
 
 template <int WM_, int WN_, int TM_, int TN_, int NR_>
 struct Tile {
@@ -110,17 +127,18 @@ struct Tile {
   static constexpr int COPIES = BUF / 1024;
   static constexpr int CPW = COPIES / WAVES;
   static_assert(COPIES % WAVES == 0, "every wave copies the same number of KB");
-  static_assert(NR == 4, "four ring buffers");
+  static_assert(NR == 2 || NR == 3, "two or three ring buffers");
   static_assert(CPW * NR < 64, "vmcnt range");
 };
 
-using Big = Tile<2, 4, 8, 4, 4>;     // 256 x 256, 8 waves, 128 KB: one workgroup per CU
-using Med = Tile<2, 2, 4, 4, 4>;     // 128 x 128, 4 waves, 64 KB: two
-using Small = Tile<2, 2, 2, 2, 4>;   //  64 x  64, 4 waves, 32 KB
+using Big = Tile<2, 4, 8, 4, 2>;     // 256 x 256, 8 waves, 128 KB: linear_turns
+using Med = Tile<2, 2, 4, 4, 2>;     // 128 x 128, 4 waves, 64 KB
+using Tall = Tile<2, 2, 4, 2, 3>;    // 128 x 64, 4 waves, 72 KB
+using Small = Tile<2, 2, 2, 2, 2>;   //  64 x 64, 4 waves, 32 KB
 
-// XOR key of the 16-byte chunks of a 64-byte LDS row: a fragment read covers
-// 16 consecutive rows, chunk lane / 16.
-__device__ inline int swz_key(int row) { return (row >> 1) & 3; }
+// XOR key of the 16-byte chunks of an LDS row: a fragment read covers 16
+// consecutive rows at one chunk, which must fill all banks.
+__device__ inline int swz_key(int row) { return (row >> 1) & (CHUNKS - 1); }
 
 // vmcnt = n (later steps' copies stay in flight), lgkmcnt = 0: this wave's LDS
 // reads are complete before the barrier lets another wave copy over them.
@@ -130,15 +148,99 @@ __device__ inline void ring_wait() {
   __builtin_amdgcn_s_waitcnt((n & 15) | ((n >> 4) << 14) | (0x7 << 4));
 }
 
+// lgkmcnt = 0 alone
+__device__ inline void lds_wait() { __builtin_amdgcn_s_waitcnt(0xC07F); }
+
+// One wave's part of a tile: its copies, fragments, accumulators and outputs.
+template <class C>
+struct Wave {
+  int m0, n0;                      // the tile
+  int lane, wave, wm, wn, fr, fk;
+  int nchunks;                     // 16-byte chunks of a row
+  const uint16_t* src[C::CPW];
+  int chunk[C::CPW];
+  int key, x_lane, w_lane;
+  f32x4 acc[C::TM][C::TN];
+
+  __device__ Wave(const LinearArgs& a, int tmi, int tni) : m0(tmi * C::BM), n0(tni * C::BN) {
+    lane = threadIdx.x & 63;
+    wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    nchunks = a.K / 8;
+    // copies of a step, 1 KB each: lane j fills physical chunk j % 8 of row j / 8.
+    // Rows past the matrix read its last row; chunks past K (the last step's)
+    // the row's last chunk, zeroed in read().
+#pragma unroll
+    for (int i = 0; i < C::CPW; ++i) {
+      const int row = (wave * C::CPW + i) * (1024 / ROWB) + lane / CHUNKS;
+      chunk[i] = (lane % CHUNKS) ^ swz_key(row);
+      src[i] = row < C::BM ? a.X + (int64_t)min(m0 + row, a.M - 1) * a.K
+                           : a.W + (int64_t)min(n0 + row - C::BM, a.N - 1) * a.K;
+    }
+    wm = wave / C::WN;
+    wn = wave - wm * C::WN;
+    fr = lane & 15;
+    fk = lane >> 4;
+    // tile t of a wave starts 16 rows further, where the swizzle key is the same
+    key = swz_key(fr);
+    x_lane = (wm * C::TM * 16 + fr) * ROWB;
+    w_lane = (C::BM + wn * C::TN * 16 + fr) * ROWB;
+#pragma unroll
+    for (int i = 0; i < C::TM; ++i)
+#pragma unroll
+      for (int j = 0; j < C::TN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+
+  __device__ void copy(int step, uint8_t* buf) {
+#pragma unroll
+    for (int i = 0; i < C::CPW; ++i) {
+      const uint16_t* g = src[i] + 8 * min(CHUNKS * step + chunk[i], nchunks - 1);
+      __builtin_amdgcn_global_load_lds(g, (lds_ptr)(buf + (wave * C::CPW + i) * 1024), 16, 0, 0);
+    }
+  }
+
+  // the fragments of half u (32 channels) of a step
+  __device__ void read(bf16x8 (&xf)[C::TM], bf16x8 (&wf)[C::TN], const uint8_t* buf, int step, int u) {
+    const int at = ((4 * u + fk) ^ key) << 4;
+#pragma unroll
+    for (int t = 0; t < C::TN; ++t) wf[t] = *reinterpret_cast<const bf16x8*>(buf + w_lane + at + t * 16 * ROWB);
+#pragma unroll
+    for (int t = 0; t < C::TM; ++t) xf[t] = *reinterpret_cast<const bf16x8*>(buf + x_lane + at + t * 16 * ROWB);
+    if (CHUNKS * (step + 1) > nchunks) {       // the matrices' last step, cut short
+      if (CHUNKS * step + 4 * u + fk >= nchunks) {
+#pragma unroll
+        for (int t = 0; t < C::TN; ++t) wf[t] = __builtin_bit_cast(bf16x8, u32x4{0u, 0u, 0u, 0u});
+#pragma unroll
+        for (int t = 0; t < C::TM; ++t) xf[t] = __builtin_bit_cast(bf16x8, u32x4{0u, 0u, 0u, 0u});
+      }
+    }
+  }
+
+  __device__ void multiply(const bf16x8 (&xf)[C::TM], const bf16x8 (&wf)[C::TN]) {
+#pragma unroll
+    for (int tm = 0; tm < C::TM; ++tm)
+#pragma unroll
+      for (int tn = 0; tn < C::TN; ++tn)
+        acc[tm][tn] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[tn], xf[tm], acc[tm][tn], 0, 0, 0);
+  }
+
+  template <class F>
+  __device__ void outputs(F&& f) {             // f(tn, n) -> g; g(acc, m)
+#pragma unroll
+    for (int tn = 0; tn < C::TN; ++tn) {
+      const int n = n0 + wn * C::TN * 16 + 16 * tn + 4 * fk;
+      auto g = f(n);
+#pragma unroll
+      for (int tm = 0; tm < C::TM; ++tm) g(acc[tm][tn], (int64_t)m0 + wm * C::TM * 16 + 16 * tm + fr);
+    }
+  }
+};
+
 template <class C, class O, int ACT, bool SHARES>
 __global__ __launch_bounds__(C::THREADS, 2) void linear_tile(const LinearArgs a) {
+  // each buffer its own array: reading one then does not wait for copies into another
   __shared__ __attribute__((aligned(16))) uint8_t ring0[C::BUF];
   __shared__ __attribute__((aligned(16))) uint8_t ring1[C::BUF];
-  __shared__ __attribute__((aligned(16))) uint8_t ring2[C::BUF];
-  __shared__ __attribute__((aligned(16))) uint8_t ring3[C::BUF];
-  const int tid = threadIdx.x;
-  const int lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  __shared__ __attribute__((aligned(16))) uint8_t ring2[C::NR > 2 ? C::BUF : 16];
   const int ntm = (a.M + C::BM - 1) / C::BM;
   const int ntn = (a.N + C::BN - 1) / C::BN;
   const int tiles = ntm * ntn;
@@ -153,98 +255,117 @@ __global__ __launch_bounds__(C::THREADS, 2) void linear_tile(const LinearArgs a)
     tail::tile_of_id(ntm, ntn, tail::xcd_compact(blockIdx.x, tiles), tmi, tni);
   }
   const int nsteps = se - sb;
-  const int m0 = tmi * C::BM, n0 = tni * C::BN;
+  Wave<C> w(a, tmi, tni);
 
-  // This wave's copies of a step: 16 rows of 64 bytes each; lane j fills
-  // physical chunk j % 4 of row j / 4.  Rows past the matrix read its last
-  // row; chunks past K (the last step's) the row's last chunk, zeroed below.
-  const int nchunks = a.K / 8;
-  const uint16_t* src[C::CPW];
-  int chunk[C::CPW];
-#pragma unroll
-  for (int i = 0; i < C::CPW; ++i) {
-    const int row = (wave * C::CPW + i) * 16 + (lane >> 2);
-    chunk[i] = (lane & 3) ^ swz_key(row);
-    src[i] = row < C::BM ? a.X + (int64_t)min(m0 + row, a.M - 1) * a.K
-                         : a.W + (int64_t)min(n0 + row - C::BM, a.N - 1) * a.K;
-  }
-  auto copy_step = [&](int s, uint8_t* buf) {
-#pragma unroll
-    for (int i = 0; i < C::CPW; ++i) {
-      const uint16_t* g = src[i] + 8 * min(4 * s + chunk[i], nchunks - 1);
-      __builtin_amdgcn_global_load_lds(g, (lds_ptr)(buf + (wave * C::CPW + i) * 1024), 16, 0, 0);
-    }
-  };
-
-  const int wm = wave / C::WN, wn = wave - wm * C::WN;
-  const int fr = lane & 15, fk = lane >> 4;
-  const int swz = (fk ^ swz_key(fr)) << 4;
-  const int x_lane = (wm * C::TM * 16 + fr) * ROWB + swz;
-  const int w_lane = (C::BM + wn * C::TN * 16 + fr) * ROWB + swz;
-  f32x4 acc[C::TM][C::TN];
-#pragma unroll
-  for (int i = 0; i < C::TM; ++i)
-#pragma unroll
-    for (int j = 0; j < C::TN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-
+  // step sb + j from `cur`; step sb + j + NR - 1 (past the last: the last
+  // again, never read) is copied to the buffer that step sb + j - 1 used
   auto step = [&](int j, const uint8_t* cur, uint8_t* freed) {
-    ring_wait<C::CPW * 2>();
+    ring_wait<C::CPW * (C::NR - 2)>();
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    copy_step(sb + min(j + 3, nsteps - 1), freed);
+    w.copy(sb + min(j + C::NR - 1, nsteps - 1), freed);
     __builtin_amdgcn_sched_barrier(0);
-    bf16x8 xf[C::TM], wf[C::TN];
 #pragma unroll
-    for (int t = 0; t < C::TN; ++t) wf[t] = *reinterpret_cast<const bf16x8*>(cur + w_lane + t * 16 * ROWB);
-#pragma unroll
-    for (int t = 0; t < C::TM; ++t) xf[t] = *reinterpret_cast<const bf16x8*>(cur + x_lane + t * 16 * ROWB);
-    if (4 * (sb + j) + 4 > nchunks) {      // the matrices' last step, cut short
-      if (4 * (sb + j) + fk >= nchunks) {
-#pragma unroll
-        for (int t = 0; t < C::TN; ++t) wf[t] = __builtin_bit_cast(bf16x8, u32x4{0u, 0u, 0u, 0u});
-#pragma unroll
-        for (int t = 0; t < C::TM; ++t) xf[t] = __builtin_bit_cast(bf16x8, u32x4{0u, 0u, 0u, 0u});
-      }
+    for (int u = 0; u < 2; ++u) {
+      bf16x8 xf[C::TM], wf[C::TN];
+      w.read(xf, wf, cur, sb + j, u);
+      w.multiply(xf, wf);
     }
-#pragma unroll
-    for (int tm = 0; tm < C::TM; ++tm)
-#pragma unroll
-      for (int tn = 0; tn < C::TN; ++tn)
-        acc[tm][tn] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[tn], xf[tm], acc[tm][tn], 0, 0, 0);
   };
-
-  copy_step(sb, ring0);
-  copy_step(sb + min(1, nsteps - 1), ring1);
-  copy_step(sb + min(2, nsteps - 1), ring2);
-  int j0 = 0;
-  for (; j0 + 4 <= nsteps; j0 += 4) {
-    step(j0, ring0, ring3);
-    step(j0 + 1, ring1, ring0);
-    step(j0 + 2, ring2, ring1);
-    step(j0 + 3, ring3, ring2);
+  w.copy(sb, ring0);
+  if constexpr (C::NR > 2) w.copy(sb + min(1, nsteps - 1), ring1);
+  // whole turns of the ring without branches, then the rest
+  int j = 0;
+  if constexpr (C::NR == 2) {
+    for (; j + 2 <= nsteps; j += 2) {
+      step(j, ring0, ring1);
+      step(j + 1, ring1, ring0);
+    }
+    if (j < nsteps) step(j, ring0, ring1);
+  } else {
+    for (; j + 3 <= nsteps; j += 3) {
+      step(j, ring0, ring2);
+      step(j + 1, ring1, ring0);
+      step(j + 2, ring2, ring1);
+    }
+    if (j < nsteps) step(j, ring0, ring2);
+    if (j + 1 < nsteps) step(j + 1, ring1, ring0);
   }
-  if (j0 < nsteps) step(j0, ring0, ring3);
-  if (j0 + 1 < nsteps) step(j0 + 1, ring1, ring0);
-  if (j0 + 2 < nsteps) step(j0 + 2, ring2, ring1);
   ring_wait<0>();     // a workgroup may not leave copies into its LDS behind
 
-  const bool wide = a.wide;
-#pragma unroll
-  for (int tm = 0; tm < C::TM; ++tm) {
-    const int64_t m = m0 + wm * C::TM * 16 + 16 * tm + fr;
-#pragma unroll
-    for (int tn = 0; tn < C::TN; ++tn) {
-      const int n = n0 + wn * C::TN * 16 + 16 * tn + 4 * fk;
-      if constexpr (SHARES) {
-        if (m < a.M && n < a.N) {
-          float* p = a.part + ((int64_t)share * a.M + m) * a.part_ld + n;   // part_ld: N rounded up to 4
-          *reinterpret_cast<f32x4*>(p) = acc[tm][tn];
-        }
-      } else {
-        finish4<O, ACT>(acc[tm][tn], a, m, n, wide);
-      }
-    }
+  if constexpr (SHARES) {
+    w.outputs([&](int n) {
+      return [&a, n, share](f32x4 v, int64_t m) {
+        if (m < a.M && n < a.N)       // part_ld: N rounded up to 4
+          *reinterpret_cast<f32x4*>(a.part + ((int64_t)share * a.M + m) * a.part_ld + n) = v;
+      };
+    });
+  } else {
+    w.outputs([&](int n) {
+      return [&a, n, bias = bias4(a, n)](f32x4 v, int64_t m) { finish4<O, ACT>(v, bias, a, m, n); };
+    });
   }
+}
+
+// The 256 x 256 tile: waves 0..3 and 4..7, one of each on every SIMD, are half a
+// turn apart, so that one group's MFMAs run while the other's LDS reads do.
+// A turn is half a step: read the fragments, barrier, multiply, barrier; the
+// second group passes one barrier more at the start, the first one more at
+// the end.  Buffers: step j + 1 is copied while step j runs, from the group's
+// first turn of j on (by then both groups have read step j - 1 whole), and
+// has landed before the barrier that ends the reading of j's second half.
+// Alone, the MFMAs and LDS reads of this loop reach 2085 TFLOP/s; the copies'
+// writes into LDS take the rest (1 of 4 cycles that the LDS has).
+template <class O, int ACT>
+__global__ __launch_bounds__(Big::THREADS, 2) void linear_turns(const LinearArgs a) {
+  using C = Big;
+  __shared__ __attribute__((aligned(16))) uint8_t ring0[C::BUF];
+  __shared__ __attribute__((aligned(16))) uint8_t ring1[C::BUF];
+  const int ntm = (a.M + C::BM - 1) / C::BM;
+  const int ntn = (a.N + C::BN - 1) / C::BN;
+  const int nsteps = (a.K + KS - 1) / KS;
+  int tmi, tni;
+  tail::tile_of_id(ntm, ntn, tail::xcd_compact(blockIdx.x, ntm * ntn), tmi, tni);
+  Wave<C> w(a, tmi, tni);
+  auto barrier = [] {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto step = [&](int j, const uint8_t* cur, uint8_t* other) {
+    w.copy(min(j + 1, nsteps - 1), other);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      bf16x8 xf[C::TM], wf[C::TN];
+      w.read(xf, wf, cur, j, u);
+      if (u == 1)
+        ring_wait<0>();
+      else
+        lds_wait();
+      barrier();
+      __builtin_amdgcn_s_setprio(1);
+      w.multiply(xf, wf);
+      __builtin_amdgcn_s_setprio(0);
+      barrier();
+    }
+  };
+  w.copy(0, ring0);
+  ring_wait<0>();
+  barrier();
+  const bool second = w.wave >= C::WAVES / 2;
+  if (second) barrier();
+  int j = 0;
+  for (; j + 2 <= nsteps; j += 2) {
+    step(j, ring0, ring1);
+    step(j + 1, ring1, ring0);
+  }
+  if (j < nsteps) step(j, ring0, ring1);
+  if (!second) barrier();
+  w.outputs([&](int n) {
+    return [&a, n, bias = bias4(a, n)](f32x4 v, int64_t m) { finish4<O, ACT>(v, bias, a, m, n); };
+  });
 }
 
 // Sums the shares in order and finishes the outputs, four per thread.
@@ -258,29 +379,28 @@ __global__ __launch_bounds__(256) void linear_join(const LinearArgs a) {
   f32x4 v = f32x4{0.f, 0.f, 0.f, 0.f};
   for (int s = 0; s < a.splits; ++s)
     v += *reinterpret_cast<const f32x4*>(a.part + ((int64_t)s * a.M + m) * a.part_ld + n);
-  finish4<O, ACT>(v, a, m, n, a.wide);
+  finish4<O, ACT>(v, bias4(a, n), a, m, n);
 }
 
-// Few rows: 16 weight rows (n) and MT x 16 rows of X per workgroup; wave w takes
-// every WAVES-th block of 64 channels.  Lane (fk, fr) reads 32 neighbouring
+// Up to 16 rows: 16 weight rows per workgroup; wave w takes every
+// kRowWaves-th block of 64 channels.  Lane (fk, fr) reads 32 neighbouring
 // bytes of weight row fr, so that the four lanes of a row take a whole
 // 128-byte line; the MFMA's k slots are any 32 channels as long as both
-// operands agree, so the two 16-byte halves are two MFMA steps.
+// operands agree, so the two 16-byte halves are two MFMAs.  (From 17 rows on the
+// tiles are faster: 32 x 3072 -> 18432 31 us in 64 x 64 tiles with two shares,
+// 54 us here with two blocks of rows.)
+constexpr int kRowsMax = 16;
 constexpr int kRowWaves = 8;
-template <class O, int ACT, int MT>
+template <class O, int ACT>
 __global__ __launch_bounds__(kRowWaves * 64) void linear_rows(const LinearArgs a) {
-  __shared__ f32x4 sums[kRowWaves][MT][64];
+  __shared__ f32x4 sums[kRowWaves][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int fr = lane & 15, fk = lane >> 4;
   const int n0 = blockIdx.x * 16;
   const uint16_t* w = a.W + (int64_t)min(n0 + fr, a.N - 1) * a.K;
-  const uint16_t* x[MT];
-#pragma unroll
-  for (int t = 0; t < MT; ++t) x[t] = a.X + (int64_t)min(16 * t + fr, a.M - 1) * a.K;
-  f32x4 acc[MT];
-#pragma unroll
-  for (int t = 0; t < MT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const uint16_t* x = a.X + (int64_t)min(fr, a.M - 1) * a.K;
+  f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
   const int blocks = (a.K + 63) / 64;
   const u32x4 zero = u32x4{0u, 0u, 0u, 0u};
 #pragma unroll 4
@@ -291,105 +411,118 @@ __global__ __launch_bounds__(kRowWaves * 64) void linear_rows(const LinearArgs a
       const int at = min(k + 8 * u, a.K - 8);
       const bool in = k + 8 * u < a.K;
       u32x4 wv = *reinterpret_cast<const u32x4*>(w + at);
+      u32x4 xv = *reinterpret_cast<const u32x4*>(x + at);
       wv = in ? wv : zero;
-#pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        u32x4 xv = *reinterpret_cast<const u32x4*>(x[t] + at);
-        xv = in ? xv : zero;
-        acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, wv),
-                                                         __builtin_bit_cast(bf16x8, xv), acc[t], 0, 0, 0);
-      }
+      xv = in ? xv : zero;
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, wv), __builtin_bit_cast(bf16x8, xv), acc,
+                                                    0, 0, 0);
     }
   }
-#pragma unroll
-  for (int t = 0; t < MT; ++t) sums[wave][t][lane] = acc[t];
+  sums[wave][lane] = acc;
   __syncthreads();
-  if (wave >= MT) return;
-  // wave t joins and finishes rows 16 t .. + 15
-  f32x4 v = sums[0][wave][lane];
+  if (wave > 0) return;
+  f32x4 v = sums[0][lane];
 #pragma unroll
-  for (int s = 1; s < kRowWaves; ++s) v += sums[s][wave][lane];
-  finish4<O, ACT>(v, a, 16 * wave + fr, n0 + 4 * fk, a.wide);
+  for (int s = 1; s < kRowWaves; ++s) v += sums[s][lane];
+  finish4<O, ACT>(v, bias4(a, n0 + 4 * fk), a, fr, n0 + 4 * fk);
 }
 
-constexpr int kRowsMax = 64;       // linear_rows: at most four blocks of 16 rows
-
-enum Kind { kKindRows, kKindBig, kKindMed, kKindSmall };
+enum Kind { kKindRows, kKindBig, kKindMed, kKindTall, kKindSmall };
 struct Plan {
-  Kind kind = kKindSmall;
+  Kind kind = kKindRows;
   int splits = 1;
   int64_t blocks = 0;
   size_t bytes = 0;
 };
 
 template <class C>
-int64_t tiles_of(int M, int N) {
-  return (int64_t)((M + C::BM - 1) / C::BM) * ((N + C::BN - 1) / C::BN);
+int64_t tiles_of(int64_t M, int64_t N) {
+  return ((M + C::BM - 1) / C::BM) * ((N + C::BN - 1) / C::BN);
 }
 
+// Tile and shares by an estimate of the time, in us: a CU that gets n tiles
+// takes max(alone, n each) for a step of 64 channels of all of them (`alone`:
+// what the copies' latency costs one tile; `each`: its part of the CU's
+// bandwidth; 128 x 128 tiles run in pairs, so an odd one costs two), and shares
+// cost a second launch and the traffic of their sums.  Measured for a step:
+// 256 x 256 1.6 alone, 1.7 each; 128 x 128 0.8 / 0.5; 128 x 64 0.31 / 0.33 (and 0.8
+// more to fill its ring); 64 x 64 0.36 / 0.19.  On 17 shapes from 925 x 440 -> 89
+// to 4608 x 12288 -> 3072 the choice is the fastest or within 10 % of it, where
+// always taking 128 x 64 loses up to 57 % and always 64 x 64 up to 96 %.
+constexpr int kMaxSplits = 8;
+constexpr int kMinShareSteps = 8;          // below that a share is all latency
+constexpr size_t kMaxPartBytes = size_t(32) << 20;
+
 Plan plan_of(int M, int K, int N) {
-  Plan p;
-  const int cus = device_cu_count();
+  Plan best;
   if (M <= kRowsMax) {
-    p.kind = kKindRows;
-    p.blocks = (N + 15) / 16;
-    return p;
+    best.blocks = ((int64_t)N + 15) / 16;
+    return best;
   }
-  if (tiles_of<Big>(M, N) >= cus) {
-    p.kind = kKindBig;
-    p.blocks = tiles_of<Big>(M, N);
-    return p;
+  const struct {
+    Kind kind;
+    int64_t tiles;
+    double alone, each, fill;
+  } tile[] = {{kKindBig, tiles_of<Big>(M, N), 1.6, 1.7, 0.0},
+              {kKindMed, tiles_of<Med>(M, N), 0.8, 0.5, 0.0},
+              {kKindTall, tiles_of<Tall>(M, N), 0.31, 0.33, 0.8},
+              {kKindSmall, tiles_of<Small>(M, N), 0.36, 0.19, 0.0}};
+  const int cus = device_cu_count();
+  const int64_t steps = ((int64_t)K + KS - 1) / KS;
+  double least = 0;
+  for (const auto& t : tile)
+    for (int s = 1; s <= (t.kind == kKindBig ? 1 : kMaxSplits); s *= 2) {
+      const size_t part = s > 1 ? (size_t)s * M * (((size_t)N + 3) / 4 * 4) * sizeof(float) : 0;
+      if (s > 1 && (steps / s < kMinShareSteps || part > kMaxPartBytes)) break;
+      int64_t n = (t.tiles * s + cus - 1) / cus;
+      if (t.kind == kKindMed && n > 1) n += n & 1;
+      double us = t.fill + (double)((steps + s - 1) / s) * std::max(t.alone, n * t.each);
+      if (s > 1) us += 3.0 + 2.0 * part / 4e6;
+      if (best.blocks == 0 || us < least) {
+        least = us;
+        best.kind = t.kind;
+        best.splits = s;
+        best.blocks = t.tiles * s;
+        best.bytes = part;
+      }
+    }
+  return best;
+}
+
+template <class C, class O, int ACT>
+hipError_t launch_tile(const Plan& p, const LinearArgs& a, hipStream_t stream) {
+  const dim3 grid((unsigned)p.blocks);
+  if (p.splits == 1) {
+    hipLaunchKernelGGL((linear_tile<C, O, ACT, false>), grid, dim3(C::THREADS), 0, stream, a);
+    return hipGetLastError();
   }
-  if (tiles_of<Med>(M, N) >= cus) {
-    p.kind = kKindMed;
-    p.blocks = tiles_of<Med>(M, N);
-    return p;
-  }
-  p.kind = kKindSmall;
-  p.blocks = tiles_of<Small>(M, N);
-  const int ksteps = (K + KS - 1) / KS;
-  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({2 * cus / p.blocks, ksteps / 16, 8}));
-  if (p.splits > 1) {
-    p.bytes = (size_t)p.splits * M * ((N + 3) / 4 * 4) * sizeof(float);
-    p.blocks *= p.splits;
-  }
-  return p;
+  // the shares do not depend on the output's type or the activation
+  hipLaunchKernelGGL((linear_tile<C, float, kActNone, true>), grid, dim3(C::THREADS), 0, stream, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int64_t quads = (int64_t)a.M * (a.part_ld / 4);
+  hipLaunchKernelGGL((linear_join<O, ACT>), dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, stream, a);
+  return hipGetLastError();
 }
 
 template <class O, int ACT>
 hipError_t launch(const Plan& p, const LinearArgs& a, hipStream_t stream) {
   const dim3 grid((unsigned)p.blocks);
   switch (p.kind) {
-    case kKindRows: {
-      const dim3 threads(kRowWaves * 64);
-      if (a.M <= 16)
-        hipLaunchKernelGGL((linear_rows<O, ACT, 1>), grid, threads, 0, stream, a);
-      else if (a.M <= 32)
-        hipLaunchKernelGGL((linear_rows<O, ACT, 2>), grid, threads, 0, stream, a);
-      else
-        hipLaunchKernelGGL((linear_rows<O, ACT, 4>), grid, threads, 0, stream, a);
+    case kKindRows:
+      hipLaunchKernelGGL((linear_rows<O, ACT>), grid, dim3(kRowWaves * 64), 0, stream, a);
       return hipGetLastError();
-    }
     case kKindBig:
-      hipLaunchKernelGGL((linear_tile<Big, O, ACT, false>), grid, dim3(Big::THREADS), 0, stream, a);
+      hipLaunchKernelGGL((linear_turns<O, ACT>), grid, dim3(Big::THREADS), 0, stream, a);
       return hipGetLastError();
     case kKindMed:
-      hipLaunchKernelGGL((linear_tile<Med, O, ACT, false>), grid, dim3(Med::THREADS), 0, stream, a);
-      return hipGetLastError();
+      return launch_tile<Med, O, ACT>(p, a, stream);
+    case kKindTall:
+      return launch_tile<Tall, O, ACT>(p, a, stream);
     case kKindSmall:
-      break;
+      return launch_tile<Small, O, ACT>(p, a, stream);
   }
-  if (p.splits == 1) {
-    hipLaunchKernelGGL((linear_tile<Small, O, ACT, false>), grid, dim3(Small::THREADS), 0, stream, a);
-    return hipGetLastError();
-  }
-  // the shares do not depend on the output's type or the activation
-  hipLaunchKernelGGL((linear_tile<Small, float, kActNone, true>), grid, dim3(Small::THREADS), 0, stream, a);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  const int64_t quads = (int64_t)a.M * (a.part_ld / 4);
-  hipLaunchKernelGGL((linear_join<O, ACT>), dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, stream, a);
-  return hipGetLastError();
+  return hipErrorInvalidValue;
 }
 
 template <class O>
@@ -408,7 +541,6 @@ hipError_t launch_linear_bf16(LinearArgs a, int act, bool fp32, hipStream_t stre
   const Plan p = plan_of(a.M, a.K, a.N);
   a.splits = p.splits;
   a.part_ld = (a.N + 3) / 4 * 4;
-  a.wide = a.N % 4 == 0;
   return fp32 ? with_act<float>(p, a, act, stream) : with_act<uint16_t>(p, a, act, stream);
 }
 

@@ -640,7 +640,7 @@ svdq_status svdq_linear_bf16_forward(const uint16_t* X, int64_t M, int K, int N,
       if (workspace_bytes < need)
         return fail(SVDQ_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", need, workspace_bytes);
     }
-    LinearArgs a = {X, W, bias, residual, Y, (int)M, K, N, static_cast<float*>(workspace), 1, 0, false};
+    LinearArgs a = {X, W, bias, residual, Y, (int)M, K, N, static_cast<float*>(workspace), 1, 0};
     return hip_check(launch_linear_bf16(a, activation, out_dtype == SVDQ_F32, static_cast<hipStream_t>(stream)),
                      "linear_bf16 launch");
   });

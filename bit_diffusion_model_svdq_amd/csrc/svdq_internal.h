@@ -205,7 +205,6 @@ struct LinearArgs {
   const uint16_t *X, *W, *bias; const void* residual; void* Y; int M, K, N;
   float* part;
   int splits, part_ld;
-  bool wide;               // rows of Y are aligned for four outputs at once
 };
 size_t linear_workspace(int M, int K, int N);
 int64_t linear_blocks(int M, int K, int N);
