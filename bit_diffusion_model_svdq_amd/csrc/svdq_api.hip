@@ -545,6 +545,8 @@ svdq_status svdq_attention_forward(const uint16_t* Q, int64_t ldq, const uint16_
     SVDQ_TRY(check_ld(ldk, wk, "ldk"));
     SVDQ_TRY(check_ld(ldv, wk, "ldv"));
     SVDQ_TRY(check_ld(ldo, wq, "ldo"));
+    if (ldk > kAttentionMaxLd || ldv > kAttentionMaxLd)
+      return fail(SVDQ_ERR_UNSUPPORTED, "ldk=%lld or ldv=%lld is above 2^24", (long long)ldk, (long long)ldv);
     SVDQ_TRY(check_ptr(Q, "Q", total_q == 0));
     SVDQ_TRY(check_ptr(K, "K", total_k == 0 || total_q == 0));
     SVDQ_TRY(check_ptr(V, "V", total_k == 0 || total_q == 0));

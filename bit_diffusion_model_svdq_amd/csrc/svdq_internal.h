@@ -162,6 +162,8 @@ struct AttentionArgs {
   float* lse;
   void* workspace;
 };
+// A tile of 32 keys is addressed by 32-bit byte offsets.
+constexpr int64_t kAttentionMaxLd = int64_t(1) << 24;
 size_t attention_workspace(int total_q, int total_k, int batch, int heads_q, int heads_kv, int head_dim);
 // The largest grid of the call's launches, in workgroups of at most 512 threads.
 int64_t attention_blocks(int total_q, int total_k, int batch, int heads_q, int heads_kv, int head_dim);

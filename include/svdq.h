@@ -399,7 +399,8 @@ size_t svdq_attention_workspace_bytes(int64_t total_q, int64_t total_k, int batc
  * j <= i + nk - nq of nk, so that the last query sees the last key.
  * A query that sees no key gets O = 0 and log-sum-exp -inf.
  * lse (float32 [heads_q, total_q], may be NULL): ln sum_j exp(scale Q . K).
- * Requires head_dim a multiple of 8 up to 128 (above: SVDQ_ERR_UNSUPPORTED),
+ * Requires head_dim a multiple of 8 up to 128 and ldk, ldv up to 2^24 (above:
+ * SVDQ_ERR_UNSUPPORTED),
  * heads_q a multiple of heads_kv, scale positive and finite.  Non-finite K or
  * V elements can reach every query of their sequence and key head, also the
  * queries that the causal mask hides them from, but no other sequence.

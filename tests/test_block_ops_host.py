@@ -33,7 +33,7 @@ def attention(**over):
     (dict(scale=0.0), INVALID), (dict(scale=-1.0), INVALID), (dict(scale=float("inf")), INVALID),
     (dict(scale=float("nan")), INVALID), (dict(causal=2), INVALID),
     (dict(ldq=504), INVALID), (dict(ldq=516), INVALID), (dict(ldk=120), INVALID), (dict(ldv=129), INVALID),
-    (dict(ldo=256), INVALID),
+    (dict(ldo=256), INVALID), (dict(ldk=(1 << 24) + 8), UNSUPPORTED), (dict(ldv=1 << 30), UNSUPPORTED),
     (dict(Q=None), INVALID), (dict(K=None), INVALID), (dict(V=None), INVALID), (dict(O=None), INVALID),
     (dict(cu_q=None), INVALID), (dict(cu_k=None), INVALID),
     (dict(Q=P + 2), ALIGNMENT), (dict(K=P + 8), ALIGNMENT), (dict(V=P + 8), ALIGNMENT), (dict(O=P + 4), ALIGNMENT),
