@@ -246,13 +246,16 @@ def _need(t, name, dtypes, shape=None, numel=None, optional=False):
         if optional:
             return
         raise ValueError(f"{name} must not be None")
-    if not hasattr(t, "data_ptr") or not hasattr(t, "is_contiguous"):
-        raise TypeError(f"{name} must be a torch tensor on the GPU")
-    if t.device.type != "cuda":
-        raise ValueError(f"{name} must live on the GPU (got device {t.device})")
-    if not t.is_contiguous():
+    try:
+        device, dtype, contiguous = t.device, t.dtype, t.is_contiguous()
+        t.data_ptr
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch tensor on the GPU") from None
+    if device.type != "cuda":
+        raise ValueError(f"{name} must live on the GPU (got device {device})")
+    if not contiguous:
         raise ValueError(f"{name} must be contiguous")
-    if dtypes is not None and _dtype_name(t) not in dtypes:
+    if dtypes is not None and (_DTYPE_NAMES.get(dtype) or _dtype_name(t)) not in dtypes:
         raise ValueError(f"{name} must have dtype {' or '.join(dtypes)} (got {_dtype_name(t)})")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
@@ -263,17 +266,13 @@ def _need(t, name, dtypes, shape=None, numel=None, optional=False):
 def _same_device(*ts):
     first = None
     for t in ts:
-        if t is None:
-            continue
-        if first is None:
-            first = t.device
-        elif t.device != first:
-            break
-    else:
-        return
-    devs = {t.device for t in ts if t is not None}
-    if len(devs) > 1:
-        raise ValueError(f"tensors live on different devices: {sorted(str(d) for d in devs)}")
+        if t is not None:
+            d = t.device
+            if first is None:
+                first = d
+            elif d != first:
+                devs = {t.device for t in ts if t is not None}
+                raise ValueError(f"tensors live on different devices: {sorted(str(d) for d in devs)}")
 
 
 def _rank_of(L1, L2=None, N=None):
@@ -617,16 +616,14 @@ def svdq_quantize_activations_mxfp4(X, smooth, L1, qx, sx_e8m0, T, stream=None):
 _BF16_F32 = _BF16 + ("float32",)
 
 
-def _launch(device, stream, name, *args):
-    """The library's function on the tensors' device, with its current stream unless one is given."""
-    index = device.index
-    if index is not None and index != _torch.cuda.current_device():
-        with _torch.cuda.device(device):
-            return _launch(device, stream, name, *args)
-    s = _current_stream(index) if stream is None else stream.cuda_stream
-    st = getattr(_lib, name)(*args, s)
+def _launch(index, stream, f, *args):
+    """The library's function f on device `index`, on its current stream unless one is given."""
+    if index != _torch.cuda.current_device():
+        with _torch.cuda.device(index):
+            return _launch(index, stream, f, *args)
+    st = f(*args, _current_stream(index) if stream is None else stream.cuda_stream)
     if st != SVDQ_OK:
-        raise SvdqError(st, name)
+        raise SvdqError(st, f.__name__)
 
 
 # the raw handle of the current stream; building torch's Stream object takes longer than a launch
@@ -634,7 +631,7 @@ _raw_stream = getattr(getattr(_torch, "_C", None), "_cuda_getCurrentRawStream", 
 
 
 def _current_stream(index):
-    if _raw_stream is not None and index is not None:
+    if _raw_stream is not None:
         return _raw_stream(index)
     return _torch.cuda.current_stream().cuda_stream
 
@@ -643,21 +640,42 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _agree(index, *checks):
+    """Whether every (tensor or None, dtypes, shape) is contiguous and as it should be on device
+    `index`: one pass over what the kernels rely on, since these calls are as short as their
+    checks.  Where it fails, the checks below say what is wrong."""
+    if index < 0:
+        return False
+    for t, dtypes, shape in checks:
+        if t is not None and not (t.get_device() == index and t.dtype in dtypes and t.shape == shape
+                                  and t.is_contiguous()):
+            return False
+    return True
+
+
+if _torch is not None:
+    _T_BF16 = (_torch.bfloat16, _torch.int16)
+    _T_F32 = (_torch.float32,)
+    _T_I32 = (_torch.int32,)
+
+
 def _need_heads(t, name, head_dim=None, rows=None, heads=None):
     """A [rows, heads, head_dim] bf16 tensor whose rows may lie apart (a column slice of a
     projection's output); returns the row stride in elements."""
-    if not hasattr(t, "data_ptr") or not hasattr(t, "stride"):
-        raise TypeError(f"{name} must be a torch tensor on the GPU")
-    if t.device.type != "cuda":
-        raise ValueError(f"{name} must live on the GPU (got device {t.device})")
-    if _dtype_name(t) not in _BF16:
+    try:
+        device, dtype, shape, strides = t.device, t.dtype, t.shape, t.stride()
+        t.data_ptr
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch tensor on the GPU") from None
+    if device.type != "cuda":
+        raise ValueError(f"{name} must live on the GPU (got device {device})")
+    if (_DTYPE_NAMES.get(dtype) or _dtype_name(t)) not in _BF16:
         raise ValueError(f"{name} must have dtype {' or '.join(_BF16)} (got {_dtype_name(t)})")
-    shape = t.shape
     if (len(shape) != 3 or (rows is not None and shape[0] != rows) or (heads is not None and shape[1] != heads)
             or (head_dim is not None and shape[2] != head_dim)):
         raise ValueError(f"{name} must have shape {(rows, heads, head_dim)} (got {tuple(shape)})")
     n, h, d = shape
-    ld, between, inner = t.stride()
+    ld, between, inner = strides
     if (d > 1 and inner != 1) or (h > 1 and between != d):
         raise ValueError(f"{name}: the heads of a row must be contiguous (strides {(ld, between, inner)})")
     return ld if n > 1 else h * d
@@ -673,7 +691,7 @@ def _need_cu(cu, name, batch=None):
 
 
 def _bytes(workspace):
-    return 0 if workspace is None else workspace.numel() * workspace.element_size()
+    return 0 if workspace is None else workspace.nbytes
 
 
 def svdq_attention_workspace_bytes(total_q: int, total_k: int, batch: int, heads_q: int, heads_kv: int,
@@ -691,36 +709,46 @@ def svdq_attention_forward(Q, K, V, cu_q, cu_k, scale, causal, O, lse=None, work
     total_k, heads_kv = K.shape[:2]
     ldv = _need_heads(V, "V", d, total_k, heads_kv)
     ldo = _need_heads(O, "O", d, total_q, heads_q)
-    batch = _need_cu(cu_q, "cu_q")
-    if (cu_q is None) != (cu_k is None) and batch > 1:
-        raise ValueError("cu_q and cu_k must both be given for more than one sequence")
-    if cu_k is not None:
-        _need_cu(cu_k, "cu_k", batch)
-    _need(lse, "lse", ("float32",), (heads_q, total_q), optional=True)
-    if workspace is not None:
-        _need(workspace, "workspace", None)
-    _same_device(Q, K, V, O, cu_q, cu_k, lse, workspace)
-    _launch(Q.device, stream, "svdq_attention_forward", _ptr(Q), ldq, _ptr(K), ldk, _ptr(V), ldv, _ptr(cu_q), _ptr(cu_k),
-            batch, total_q, total_k, heads_q, heads_kv, d, scale, int(causal), _ptr(O), ldo, _ptr(lse), _ptr(workspace),
-            _bytes(workspace))
+    batch = 1 if cu_q is None else cu_q.shape[0] - 1
+    index = Q.get_device()
+    if not (_agree(index, (cu_q, _T_I32, (batch + 1,)), (cu_k, _T_I32, (batch + 1,)), (lse, _T_F32, (heads_q, total_q)))
+            and K.get_device() == index and V.get_device() == index and O.get_device() == index and batch >= 1
+            and (batch == 1 or cu_k is not None) and (workspace is None or workspace.get_device() == index)):
+        batch = _need_cu(cu_q, "cu_q")
+        if (cu_q is None) != (cu_k is None) and batch > 1:
+            raise ValueError("cu_q and cu_k must both be given for more than one sequence")
+        if cu_k is not None:
+            _need_cu(cu_k, "cu_k", batch)
+        _need(lse, "lse", ("float32",), (heads_q, total_q), optional=True)
+        _same_device(Q, K, V, O, cu_q, cu_k, lse, workspace)
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    _launch(index, stream, _lib.svdq_attention_forward, Q.data_ptr(), ldq, K.data_ptr(), ldk, V.data_ptr(), ldv,
+            _ptr(cu_q), _ptr(cu_k), batch, total_q, total_k, heads_q, heads_kv, d, scale, int(causal), O.data_ptr(), ldo,
+            _ptr(lse), _ptr(workspace), _bytes(workspace))
     return O
 
 
-def _need_vectors(t, name, batch, width):
-    """Per-sequence bf16 vectors [batch, width] whose rows may lie apart; returns the row stride."""
+def _need_vectors(t, name, batch, width, index):
+    """Per-sequence bf16 vectors [batch, width] on device `index` whose rows may lie apart; returns
+    the row stride."""
     if t is None:
         return 0
-    if not hasattr(t, "data_ptr") or not hasattr(t, "stride"):
-        raise TypeError(f"{name} must be a torch tensor on the GPU")
+    try:
+        device, shape, strides = t.get_device(), t.shape, t.stride()
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch tensor on the GPU") from None
     if t.device.type != "cuda":
         raise ValueError(f"{name} must live on the GPU (got device {t.device})")
-    if _dtype_name(t) not in _BF16:
+    if (_DTYPE_NAMES.get(t.dtype) or _dtype_name(t)) not in _BF16:
         raise ValueError(f"{name} must have dtype {' or '.join(_BF16)} (got {_dtype_name(t)})")
-    if t.shape != (batch, width):
-        raise ValueError(f"{name} must have shape {(batch, width)} (got {tuple(t.shape)})")
-    if t.stride(1) != 1:
-        raise ValueError(f"{name}: the channels of a row must be contiguous (strides {tuple(t.stride())})")
-    return t.stride(0) if batch > 1 else width
+    if shape != (batch, width):
+        raise ValueError(f"{name} must have shape {(batch, width)} (got {tuple(shape)})")
+    if device != index:
+        raise ValueError(f"tensors live on different devices: {name} on {t.device}")
+    if strides[1] != 1:
+        raise ValueError(f"{name}: the channels of a row must be contiguous (strides {strides})")
+    return strides[0] if batch > 1 else width
 
 
 def svdq_block_norm_forward(x, y, cu, post, post_weight, gate, residual_scale, branch_scale, pre, pre_weight, pre_bias,
@@ -732,20 +760,28 @@ def svdq_block_norm_forward(x, y, cu, post, post_weight, gate, residual_scale, b
     Absent operands are None; x_out may be x and h may be y."""
     if x.dim() != 2:
         raise ValueError("x must be a [rows, width] tensor")
-    rows, width = x.shape
-    _need(x, "x", _BF16_F32)
+    rows, width = shape = x.shape
+    batch = 1 if cu is None else cu.shape[0] - 1
+    index = x.get_device()
     f32 = _dtype_name(x) == "float32"
-    _need(x_out, "x_out", ("float32",) if f32 else _BF16, (rows, width), optional=True)
-    _need(y, "y", _BF16, (rows, width), optional=True)
-    _need(h, "h", _BF16, (rows, width), optional=True)
-    batch = _need_cu(cu, "cu")
-    for t, name in ((post_weight, "post_weight"), (pre_weight, "pre_weight"), (pre_bias, "pre_bias")):
-        _need(t, name, _BF16, (width,), optional=True)
-    ld = [_need_vectors(t, name, batch, width) for t, name in ((gate, "gate"), (scale, "scale"), (shift, "shift"))]
-    _same_device(x, y, cu, post_weight, gate, pre_weight, pre_bias, scale, shift, x_out, h)
-    _launch(x.device, stream, "svdq_block_norm_forward", _ptr(x), SVDQ_F32 if f32 else SVDQ_BF16, _ptr(y), rows, width,
-            _ptr(cu), batch, post, _ptr(post_weight), _ptr(gate), ld[0], residual_scale, branch_scale, pre,
-            _ptr(pre_weight), _ptr(pre_bias), _ptr(scale), ld[1], _ptr(shift), ld[2], eps, _ptr(x_out), _ptr(h))
+    stream_types = _T_F32 if f32 else _T_BF16
+    if not (_agree(index, (x, stream_types, shape), (y, _T_BF16, shape), (x_out, stream_types, shape), (h, _T_BF16, shape),
+                   (cu, _T_I32, (batch + 1,)), (post_weight, _T_BF16, (width,)), (pre_weight, _T_BF16, (width,)),
+                   (pre_bias, _T_BF16, (width,))) and batch >= 1):
+        _need(x, "x", _BF16_F32)
+        _need(x_out, "x_out", ("float32",) if f32 else _BF16, (rows, width), optional=True)
+        _need(y, "y", _BF16, (rows, width), optional=True)
+        _need(h, "h", _BF16, (rows, width), optional=True)
+        batch = _need_cu(cu, "cu")
+        for t, name in ((post_weight, "post_weight"), (pre_weight, "pre_weight"), (pre_bias, "pre_bias")):
+            _need(t, name, _BF16, (width,), optional=True)
+        _same_device(x, y, cu, post_weight, pre_weight, pre_bias, x_out, h)
+    ld_gate = _need_vectors(gate, "gate", batch, width, index)
+    ld_scale = _need_vectors(scale, "scale", batch, width, index)
+    ld_shift = _need_vectors(shift, "shift", batch, width, index)
+    _launch(index, stream, _lib.svdq_block_norm_forward, x.data_ptr(), SVDQ_F32 if f32 else SVDQ_BF16, _ptr(y), rows,
+            width, _ptr(cu), batch, post, _ptr(post_weight), _ptr(gate), ld_gate, residual_scale, branch_scale, pre,
+            _ptr(pre_weight), _ptr(pre_bias), _ptr(scale), ld_scale, _ptr(shift), ld_shift, eps, _ptr(x_out), _ptr(h))
     return x_out, h
 
 
@@ -760,15 +796,20 @@ def svdq_linear_bf16_forward(X, W, bias, activation, residual, Y, workspace=None
         raise ValueError("X must be a [M, K] and W a [N, K] tensor")
     M, K = X.shape
     N = W.shape[0]
-    _need(X, "X", _BF16)
-    _need(W, "W", _BF16, (N, K))
-    _need(bias, "bias", _BF16, (N,), optional=True)
-    _need(Y, "Y", _BF16_F32, (M, N))
+    index = X.get_device()
     f32 = _dtype_name(Y) == "float32"
-    _need(residual, "residual", ("float32",) if f32 else _BF16, (M, N), optional=True)
-    if workspace is not None:
-        _need(workspace, "workspace", None)
-    _same_device(X, W, bias, residual, Y, workspace)
-    _launch(X.device, stream, "svdq_linear_bf16_forward", _ptr(X), M, K, N, _ptr(W), _ptr(bias), int(activation),
-            _ptr(residual), _ptr(Y), SVDQ_F32 if f32 else SVDQ_BF16, _ptr(workspace), _bytes(workspace))
+    out_types = _T_F32 if f32 else _T_BF16
+    if not (_agree(index, (X, _T_BF16, (M, K)), (W, _T_BF16, (N, K)), (bias, _T_BF16, (N,)), (Y, out_types, (M, N)),
+                   (residual, out_types, (M, N))) and (workspace is None or workspace.get_device() == index)):
+        _need(X, "X", _BF16)
+        _need(W, "W", _BF16, (N, K))
+        _need(bias, "bias", _BF16, (N,), optional=True)
+        _need(Y, "Y", _BF16_F32, (M, N))
+        _need(residual, "residual", ("float32",) if f32 else _BF16, (M, N), optional=True)
+        _same_device(X, W, bias, residual, Y, workspace)
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    _launch(index, stream, _lib.svdq_linear_bf16_forward, X.data_ptr(), M, K, N, W.data_ptr(), _ptr(bias),
+            int(activation), _ptr(residual), Y.data_ptr(), SVDQ_F32 if f32 else SVDQ_BF16, _ptr(workspace),
+            _bytes(workspace))
     return Y

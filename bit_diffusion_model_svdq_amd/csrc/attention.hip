@@ -714,20 +714,25 @@ __global__ __launch_bounds__(256) void attention_join(const Params p, int rows_p
   const int d = 2 * lane;
   const bool on = d < p.head_dim;
   float a0 = 0.f, a1 = 0.f;
-  for (int s0 = 0; s0 < shares; s0 += 8) {
-    float2 v[8];
+  auto add = [&](auto count, int s0) {
+    constexpr int N = decltype(count)::value;
+    float2 v[N];
 #pragma unroll
-    for (int u = 0; u < 8; ++u)
-      v[u] = *reinterpret_cast<const float2*>(p.part + slot(min(s0 + u, shares - 1)) * p.head_dim + (on ? d : 0));
+    for (int u = 0; u < N; ++u)
+      v[u] = *reinterpret_cast<const float2*>(p.part + slot(s0 + u) * p.head_dim + (on ? d : 0));
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const float w = s0 + u < shares ? __shfl(weight, s0 + u) : 0.f;
+    for (int u = 0; u < N; ++u) {
+      const float w = __shfl(weight, s0 + u);
       if (w > 0.f) {                                     // a share without weight has written nothing
         a0 = __builtin_fmaf(w, v[u].x, a0);
         a1 = __builtin_fmaf(w, v[u].y, a1);
       }
     }
-  }
+  };
+  int s0 = 0;
+  for (; s0 + 8 <= shares; s0 += 8) add(std::integral_constant<int, 8>{}, s0);
+  for (; s0 + 2 <= shares; s0 += 2) add(std::integral_constant<int, 2>{}, s0);
+  if (s0 < shares) add(std::integral_constant<int, 1>{}, s0);
   const float inv = sum > 0.f ? 1.f / sum : 0.f;
   if (on) {
     const uint16_t x = __builtin_bit_cast(uint16_t, (__bf16)(a0 * inv));
@@ -781,9 +786,9 @@ Plan plan_of(int total_q, int total_k, int batch, int heads_q, int heads_kv, int
   // Shares of the keys where the tiles leave CUs idle: of 128 keys at least for
   // attention_rows; for attention_keys as many as give the two workgroups of a
   // CU one share each on average, 256 keys at least, and short sequences in one.
-  // A launch holds at most 8 workgroups per CU for them (2 of attention_rows).
+  // A launch holds at most 4 workgroups per CU for them (2 of attention_rows).
   const int64_t units = pl.tiles * heads_kv;
-  const int64_t want = (pl.keys ? 8 : 8 / pl.waves) * cus / std::max<int64_t>(units, 1);
+  const int64_t want = (pl.keys ? 4 : 8 / pl.waves) * cus / std::max<int64_t>(units, 1);
   pl.chunk = 128;
   if (pl.keys) pl.chunk = (int)std::max<int64_t>(256, ((int64_t)total_k * heads_kv / (2 * cus) + 127) / 128 * 128);
   const int64_t most = ((int64_t)total_k + pl.chunk - 1) / pl.chunk;
