@@ -24,9 +24,9 @@
 //                 wave streams its share of the channels of 16 weight rows
 //                 straight into registers.
 //
-// Measured: 4608 x 3072 -> 12288 330 us (1053 TFLOP/s) with 256 x 256 turns, 347
-// with the same tile in one group, 357 / 442 / 501 with the smaller tiles;
-// 1155 x 1288 -> 1290 16.2 us with 128 x 64, 16.8 with 64 x 64, 27 with 128 x 128;
+// Measured: 4608 x 3072 -> 12288 300 us (1160 TFLOP/s) with 256 x 256 turns; with
+// bf16 stored straight from the accumulators 330 us, 347 with the same tile in
+// one group, 357 / 442 / 501 with the smaller tiles; 1155 x 1288 -> 1290 16.2 us with 128 x 64, 16.8 with 64 x 64, 27 with 128 x 128;
 // 2 x 3072 -> 18432 23.7 us (4.8 TB/s) in linear_rows.
 #include <algorithm>
 
@@ -60,6 +60,7 @@ __device__ inline float activate(float v) {
 // 16-byte boundary, and the memory pipeline takes such accesses whole.
 typedef f32x4 f32x4u __attribute__((aligned(4)));
 typedef u32x2 u32x2u __attribute__((aligned(2)));
+typedef u32x4 u32x4u __attribute__((aligned(2)));
 
 __device__ inline f32x4 unpack4(u32x2 b) {
   return f32x4{__uint_as_float(b[0] << 16), __uint_as_float(b[0] & 0xFFFF0000u), __uint_as_float(b[1] << 16),
@@ -76,40 +77,60 @@ __device__ inline f32x4 bias4(const LinearArgs& a, int n) {
   return v;
 }
 
-// Four neighbouring outputs n .. n + 3 of row m: bias, activation, residual,
-// rounding, store.
+// Four neighbouring outputs n .. n + 3 of row m in float32: bias, activation and
+// residual (of elements inside the matrix; the others are anything).
 template <class O, int ACT>
-__device__ inline void finish4(f32x4 v, f32x4 bias, const LinearArgs& a, int64_t m, int n) {
-  if (m >= a.M || n >= a.N) return;
-  const int64_t at = m * a.N + n;
-  O* y = static_cast<O*>(a.Y) + at;
-  const O* r = a.residual ? static_cast<const O*>(a.residual) + at : nullptr;
+__device__ inline f32x4 value4(f32x4 v, f32x4 bias, const LinearArgs& a, int64_t m, int n) {
   v += bias;
 #pragma unroll
   for (int i = 0; i < 4; ++i) v[i] = activate<ACT>(v[i]);
-  if (n + 4 <= a.N) {
-    if constexpr (sizeof(O) == 4) {
-      if (r) v += *reinterpret_cast<const f32x4u*>(r);
-      *reinterpret_cast<f32x4u*>(y) = v;
-    } else {
-      if (r) v += unpack4(*reinterpret_cast<const u32x2u*>(r));
-      u32x2 w;
+  if (!a.residual || m >= a.M || n >= a.N) return v;
+  const O* r = static_cast<const O*>(a.residual) + m * a.N + n;
+  if constexpr (sizeof(O) == 4) {
+    if (n + 4 <= a.N) return v + *reinterpret_cast<const f32x4u*>(r);
+    for (int i = 0; i < 4; ++i)
+      if (n + i < a.N) v[i] += r[i];
+  } else {
+    if (n + 4 <= a.N) return v + unpack4(*reinterpret_cast<const u32x2u*>(r));
+    for (int i = 0; i < 4; ++i)
+      if (n + i < a.N) v[i] += bf16_value(r[i]);
+  }
+  return v;
+}
+
+__device__ inline u32x2 pack4(f32x4 v) {
+  u32x2 w;
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        w[i] = __builtin_bit_cast(uint16_t, (__bf16)v[2 * i]) |
-               ((uint32_t)__builtin_bit_cast(uint16_t, (__bf16)v[2 * i + 1]) << 16);
-      *reinterpret_cast<u32x2u*>(y) = w;
-    }
+  for (int i = 0; i < 2; ++i)
+    w[i] = __builtin_bit_cast(uint16_t, (__bf16)v[2 * i]) |
+           ((uint32_t)__builtin_bit_cast(uint16_t, (__bf16)v[2 * i + 1]) << 16);
+  return w;
+}
+
+template <class O>
+__device__ inline void store4(f32x4 v, const LinearArgs& a, int64_t m, int n) {
+  if (m >= a.M || n >= a.N) return;
+  O* y = static_cast<O*>(a.Y) + m * a.N + n;
+  if (n + 4 <= a.N) {
+    if constexpr (sizeof(O) == 4)
+      *reinterpret_cast<f32x4u*>(y) = v;
+    else
+      *reinterpret_cast<u32x2u*>(y) = pack4(v);
     return;
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if (n + i >= a.N) break;
     if constexpr (sizeof(O) == 4)
-      y[i] = r ? v[i] + r[i] : v[i];
+      y[i] = v[i];
     else
-      y[i] = __builtin_bit_cast(uint16_t, (__bf16)(r ? v[i] + bf16_value(r[i]) : v[i]));
+      y[i] = __builtin_bit_cast(uint16_t, (__bf16)v[i]);
   }
+}
+
+template <class O, int ACT>
+__device__ inline void finish4(f32x4 v, f32x4 bias, const LinearArgs& a, int64_t m, int n) {
+  store4<O>(value4<O, ACT>(v, bias, a, m, n), a, m, n);
 }
 
 constexpr int KS = 64;            // channels per step: two MFMAs deep
@@ -126,6 +147,8 @@ struct Tile {
   static constexpr int BUF = (BM + BN) * ROWB;
   static constexpr int COPIES = BUF / 1024;
   static constexpr int CPW = COPIES / WAVES;
+  static constexpr int PITCH = 16 * TN + 8;             // bf16 of a staged output row
+  static constexpr int STAGE = WAVES * 16 * PITCH * 2;  // bytes: 16 rows per wave
   static_assert(COPIES % WAVES == 0, "every wave copies the same number of KB");
   static_assert(NR == 2 || NR == 3, "two or three ring buffers");
   static_assert(CPW * NR < 64, "vmcnt range");
@@ -223,14 +246,74 @@ struct Wave {
         acc[tm][tn] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[tn], xf[tm], acc[tm][tn], 0, 0, 0);
   }
 
-  template <class F>
-  __device__ void outputs(F&& f) {             // f(tn, n) -> g; g(acc, m)
+  // The wave's outputs.  float32 goes straight from the accumulators (64
+  // neighbouring bytes of a row per instruction); bf16 through the wave's own
+  // staging rows, 16 rows at a time, so that whole lines are stored, which then
+  // stream out non-temporally: 4608 x 3072 -> 12288 300 us, against 306 with
+  // stores that allocate in the caches and 330 with 8-byte stores straight from
+  // the accumulators.
+  template <class O, int ACT>
+  __device__ void outputs(const LinearArgs& a, uint8_t* stage) {
+    const int n1 = n0 + wn * C::TN * 16;
+    const int64_t m1 = (int64_t)m0 + wm * C::TM * 16;
+    f32x4 bias[C::TN];
+#pragma unroll
+    for (int tn = 0; tn < C::TN; ++tn) bias[tn] = bias4(a, n1 + 16 * tn + 4 * fk);
+    if constexpr (sizeof(O) == 4) {
+#pragma unroll
+      for (int tm = 0; tm < C::TM; ++tm)
+#pragma unroll
+        for (int tn = 0; tn < C::TN; ++tn)
+          finish4<O, ACT>(acc[tm][tn], bias[tn], a, m1 + 16 * tm + fr, n1 + 16 * tn + 4 * fk);
+    } else {
+      uint16_t* rows = reinterpret_cast<uint16_t*>(stage) + wave * 16 * C::PITCH;
+      constexpr int CPR = 2 * C::TN;      // 16-byte chunks of a row
+#pragma unroll
+      for (int tm = 0; tm < C::TM; ++tm) {
+#pragma unroll
+        for (int tn = 0; tn < C::TN; ++tn) {
+          const f32x4 v = value4<O, ACT>(acc[tm][tn], bias[tn], a, m1 + 16 * tm + fr, n1 + 16 * tn + 4 * fk);
+          *reinterpret_cast<u32x2*>(rows + fr * C::PITCH + 16 * tn + 4 * fk) = pack4(v);
+        }
+        // a wave's LDS accesses complete in issue order; the fences keep the
+        // compiler's order of the writes, the reads and the next pass's writes
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+#pragma unroll
+        for (int c = lane; c < 16 * CPR; c += 64) {
+          const int row = c / CPR, ch = c - (c / CPR) * CPR;
+          const int64_t m = m1 + 16 * tm + row;
+          const int n = n1 + 8 * ch;
+          const u32x4 v = *reinterpret_cast<const u32x4*>(rows + row * C::PITCH + 8 * ch);
+          if (m < a.M && n < a.N) {
+            uint16_t* y = static_cast<uint16_t*>(a.Y) + m * a.N + n;
+            if (n + 8 <= a.N) {
+              __builtin_nontemporal_store(v, reinterpret_cast<u32x4u*>(y));
+            } else {
+              for (int i = 0; i < 8; ++i)
+                if (n + i < a.N) y[i] = (uint16_t)(v[i >> 1] >> (16 * (i & 1)));
+            }
+          }
+        }
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+      }
+    }
+  }
+
+  // A share's sums, for linear_join; part_ld: N rounded up to 4.
+  __device__ void sums(const LinearArgs& a, int share) {
 #pragma unroll
     for (int tn = 0; tn < C::TN; ++tn) {
       const int n = n0 + wn * C::TN * 16 + 16 * tn + 4 * fk;
-      auto g = f(n);
 #pragma unroll
-      for (int tm = 0; tm < C::TM; ++tm) g(acc[tm][tn], (int64_t)m0 + wm * C::TM * 16 + 16 * tm + fr);
+      for (int tm = 0; tm < C::TM; ++tm) {
+        const int64_t m = (int64_t)m0 + wm * C::TM * 16 + 16 * tm + fr;
+        if (m < a.M && n < a.N)
+          *reinterpret_cast<f32x4*>(a.part + ((int64_t)share * a.M + m) * a.part_ld + n) = acc[tm][tn];
+      }
     }
   }
 };
@@ -241,6 +324,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void linear_tile(const LinearArgs a)
   __shared__ __attribute__((aligned(16))) uint8_t ring0[C::BUF];
   __shared__ __attribute__((aligned(16))) uint8_t ring1[C::BUF];
   __shared__ __attribute__((aligned(16))) uint8_t ring2[C::NR > 2 ? C::BUF : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t stage[SHARES || sizeof(O) == 4 ? 16 : C::STAGE];
   const int ntm = (a.M + C::BM - 1) / C::BM;
   const int ntn = (a.N + C::BN - 1) / C::BN;
   const int tiles = ntm * ntn;
@@ -293,18 +377,10 @@ __global__ __launch_bounds__(C::THREADS, 2) void linear_tile(const LinearArgs a)
   }
   ring_wait<0>();     // a workgroup may not leave copies into its LDS behind
 
-  if constexpr (SHARES) {
-    w.outputs([&](int n) {
-      return [&a, n, share](f32x4 v, int64_t m) {
-        if (m < a.M && n < a.N)       // part_ld: N rounded up to 4
-          *reinterpret_cast<f32x4*>(a.part + ((int64_t)share * a.M + m) * a.part_ld + n) = v;
-      };
-    });
-  } else {
-    w.outputs([&](int n) {
-      return [&a, n, bias = bias4(a, n)](f32x4 v, int64_t m) { finish4<O, ACT>(v, bias, a, m, n); };
-    });
-  }
+  if constexpr (SHARES)
+    w.sums(a, share);
+  else
+    w.template outputs<O, ACT>(a, stage);
 }
 
 // The 256 x 256 tile: waves 0..3 and 4..7, one of each on every SIMD, are half a
@@ -314,13 +390,16 @@ __global__ __launch_bounds__(C::THREADS, 2) void linear_tile(const LinearArgs a)
 // the end.  Buffers: step j + 1 is copied while step j runs, from the group's
 // first turn of j on (by then both groups have read step j - 1 whole), and
 // has landed before the barrier that ends the reading of j's second half.
-// Alone, the MFMAs and LDS reads of this loop reach 2085 TFLOP/s; the copies'
-// writes into LDS take the rest (1 of 4 cycles that the LDS has).
+// Alone, the MFMAs and LDS reads of this loop reach 2085 TFLOP/s, the copies
+// 12 TB/s; together 8192 x 8192 -> 8192 takes 791 us (1389 TFLOP/s).  Halving the
+// tiles of a last round that leaves most CUs idle gains nothing (305 us either
+// way at 4608 x 3072 -> 12288, 3.4 rounds): the tiles of such a round run faster.
 template <class O, int ACT>
 __global__ __launch_bounds__(Big::THREADS, 2) void linear_turns(const LinearArgs a) {
   using C = Big;
   __shared__ __attribute__((aligned(16))) uint8_t ring0[C::BUF];
   __shared__ __attribute__((aligned(16))) uint8_t ring1[C::BUF];
+  __shared__ __attribute__((aligned(16))) uint8_t stage[sizeof(O) == 4 ? 16 : C::STAGE];
   const int ntm = (a.M + C::BM - 1) / C::BM;
   const int ntn = (a.N + C::BN - 1) / C::BN;
   const int nsteps = (a.K + KS - 1) / KS;
@@ -363,9 +442,7 @@ __global__ __launch_bounds__(Big::THREADS, 2) void linear_turns(const LinearArgs
   }
   if (j < nsteps) step(j, ring0, ring1);
   if (!second) barrier();
-  w.outputs([&](int n) {
-    return [&a, n, bias = bias4(a, n)](f32x4 v, int64_t m) { finish4<O, ACT>(v, bias, a, m, n); };
-  });
+  w.template outputs<O, ACT>(a, stage);
 }
 
 // Sums the shares in order and finishes the outputs, four per thread.
