@@ -26,6 +26,9 @@ back-to-back launches of that kernel alone over the same rotating buffers.
 MLP up 3072 -> 12288 with GELU fused into its epilogue, MLP down
 12288 -> 3072 reading the up projection's output), each branch widened by a
 seeded rank-16 LoRA to r = 48; the attention itself is not part of it.
+--workload dit_block_full times the whole block: the modulation linear (bf16), norm and
+modulation, those four linears, attention with 24 heads of 128 channels over the fused QKV
+output, and the two calls of gate, residual (and norm) between them.
 """
 from __future__ import annotations
 
@@ -191,6 +194,8 @@ def main():
 
     if args.workload == "dit_block":
         return bench_block(args, S, synth, torch)
+    if args.workload == "dit_block_full":
+        return bench_block_full(args, S, synth, torch)
     w = synth.WORKLOADS[args.workload]
     M, K, N, r = (args.tokens or w.M), w.K, w.N, w.rank
     dev = torch.device("cuda:0")
@@ -449,16 +454,8 @@ BLOCK = (("qkv", "dit_qkv", "none", "X"), ("out", "dit_out", "none", "X"),
          ("up", "mlp_up", "gelu_tanh", "X"), ("down", "mlp_down", "none", "H"))
 
 
-def bench_block(args, S, synth, torch):
-    mx = args.format == "mxfp4"
-    dev = torch.device("cuda:0")
-
-    def t(a):
-        a = np.ascontiguousarray(a)
-        return torch.from_numpy(a.view(np.int16) if a.dtype == np.uint16 else a).to(dev)
-
-    # ---- offline pack of the four layers (host, untimed): library packer, LoRA appended
-    t0 = time.time()
+def pack_block(S, synth, mx):
+    """The four layers of the block packed on the host by the library, LoRA appended."""
     layers = []
     for name, wname, act, src in BLOCK:
         w = synth.WORKLOADS[wname]
@@ -473,6 +470,20 @@ def bench_block(args, S, synth, torch):
         X = synth.activations(w) if src == "X" else None
         layers.append(dict(name=name, w=w, act=act, src=src, M=w.M, K=w.K, N=w.N, r=L1.shape[0], X=X,
                            pk=dict(pk, L1=L1, L2=L2), b=synth.bias(w)))
+    return layers
+
+
+def bench_block(args, S, synth, torch):
+    mx = args.format == "mxfp4"
+    dev = torch.device("cuda:0")
+
+    def t(a):
+        a = np.ascontiguousarray(a)
+        return torch.from_numpy(a.view(np.int16) if a.dtype == np.uint16 else a).to(dev)
+
+    # ---- offline pack of the four layers (host, untimed): library packer, LoRA appended
+    t0 = time.time()
+    layers = pack_block(S, synth, mx)
     pack_s = time.time() - t0
     print(f"# packed dit_block in {pack_s:.1f}s", file=sys.stderr, flush=True)
     M = layers[0]["M"]
@@ -601,6 +612,142 @@ def bench_block(args, S, synth, torch):
     if not args.no_cpu_baseline:
         out["cpu_baseline"] = cpu_baseline_block(layers, args.cpu_seconds, mx)
     print(json.dumps(out), flush=True)
+
+
+def bench_block_full(args, S, synth, torch):
+    """The whole DiT block on one image: the linears' seeded layers, with a bf16 residual stream
+    and the modulation linear drawn here.  Scores stay of ordinary size: each token's QKV rows
+    come out of the packed projection on normalised, modulated rows."""
+    mx = args.format == "mxfp4"
+    dev = torch.device("cuda:0")
+    bf16 = torch.bfloat16
+
+    def t(a):
+        a = np.ascontiguousarray(a)
+        return torch.from_numpy(a.view(np.int16) if a.dtype == np.uint16 else a).to(dev)
+
+    t0 = time.time()
+    layers = pack_block(S, synth, mx)
+    pack_s = time.time() - t0
+    print(f"# packed dit_block_full in {pack_s:.1f}s", file=sys.stderr, flush=True)
+    M, C, D = layers[0]["M"], layers[0]["K"], 128
+    heads = C // D
+    wsb = S.svdq_forward_workspace_bytes_mxfp4 if mx else S.svdq_forward_workspace_bytes
+    forward = S.svdq_linear_forward_act_mxfp4 if mx else S.svdq_linear_forward_act
+    acts = {"none": S.SVDQ_ACT_NONE, "gelu_tanh": S.SVDQ_ACT_GELU_TANH}
+    ws_bytes = max([wsb(L["M"], L["K"], L["N"], L["r"]) for L in layers]
+                   + [S.svdq_attention_workspace_bytes(M, M, 1, heads, heads, D),
+                      S.svdq_linear_bf16_workspace_bytes(1, C, 6 * C)])
+    per_set = ws_bytes + 2 * M * C * 5 + 12 * C * C
+    for L in layers:
+        per_set += (L["M"] * L["N"] * 2 + L["N"] * L["K"] // 2 + L["pk"]["w_scales"].nbytes
+                    + L["r"] * (L["K"] + L["N"]) * 2)
+    nsets = max(2, -(-args.rotate_mb * (1 << 20) // per_set))
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(20241107)
+
+    def normal(*shape, std=1.0):
+        return (torch.randn(*shape, generator=gen, device=dev) * std).to(bf16)
+
+    sets = []
+    for i in range(nsets):
+        d = dict(x=normal(M, C, std=2.0), e=normal(1, C), Wm=normal(6 * C, C, std=0.3 * C**-0.5),
+                 bm=normal(6 * C, std=0.1), mod=torch.empty(1, 6 * C, dtype=bf16, device=dev),
+                 a=torch.empty(M, heads, D, dtype=bf16, device=dev), work=torch.empty(ws_bytes, dtype=torch.uint8, device=dev))
+        d["h"], d["x1"], d["x2"] = (torch.empty(M, C, dtype=bf16, device=dev) for _ in range(3))
+        for L in layers:
+            wsc = L["pk"]["w_scales"]
+            d[L["name"]] = dict(s=t(L["pk"]["smooth"]), L1=t(L["pk"]["L1"]), L2=t(L["pk"]["L2"]), Wq=t(L["pk"]["Wq"]),
+                                ws=t(S.svdq_mxfp4_tile_scales(wsc) if mx else wsc), b=t(L["b"]), act=acts[L["act"]],
+                                Y=torch.empty((M, L["N"]), dtype=torch.int16, device=dev))
+        sets.append(d)
+    torch.cuda.synchronize()
+
+    def svdq(d, name, X):
+        e = d[name]
+        forward(X.view(torch.int16), e["s"], e["L1"], e["L2"], e["Wq"], e["ws"], e["b"], e["act"], e["Y"], d["work"])
+        return e["Y"].view(bf16)
+
+    def attention(d):
+        v = d["qkv"]["Y"].view(bf16).view(M, 3 * heads, D)
+        S.svdq_attention_forward(v[:, :heads], v[:, heads:2 * heads], v[:, 2 * heads:], None, None, D**-0.5, False,
+                                 d["a"], None, d["work"])
+
+    def norm(d, x, y, gate, scale, shift, x_out, h):
+        S.svdq_block_norm_forward(x, y, None, S.SVDQ_NORM_NONE, None, gate, 1.0, 1.0,
+                                  S.SVDQ_NORM_NONE if h is None else S.SVDQ_NORM_LAYER, None, None, scale, shift,
+                                  1e-6, x_out, h)
+
+    STEPS = ("modulation", "norm", "qkv", "attention", "out", "gate_norm", "up", "down", "gate")
+
+    def run(d, ev=None):
+        sh1, sc1, g1, sh2, sc2, g2 = d["mod"].split(C, dim=1)
+        calls = (
+            lambda: S.svdq_linear_bf16_forward(d["e"], d["Wm"], d["bm"], S.SVDQ_ACT_NONE, None, d["mod"], d["work"]),
+            lambda: norm(d, d["x"], None, None, sc1, sh1, None, d["h"]),
+            lambda: svdq(d, "qkv", d["h"]),
+            lambda: attention(d),
+            lambda: svdq(d, "out", d["a"].view(M, C)),
+            lambda: norm(d, d["x"], d["out"]["Y"].view(bf16), g1, sc2, sh2, d["x1"], d["h"]),
+            lambda: svdq(d, "up", d["h"]),
+            lambda: svdq(d, "down", d["up"]["Y"]),
+            lambda: norm(d, d["x1"], d["down"]["Y"].view(bf16), g2, None, None, d["x2"], None))
+        for j, call in enumerate(calls):
+            if ev is not None:
+                ev[j].record()
+            call()
+        if ev is not None:
+            ev[len(calls)].record()
+
+    settle_n, settle_ms = settle(torch, lambda i: run(sets[i % nsets]), args.settle_ms)
+    for i in range(args.warmup):
+        run(sets[i % nsets])
+    torch.cuda.synchronize()
+    assert all(bool(torch.isfinite(d["x2"]).all()) for d in sets[:max(1, min(args.warmup, nsets))])
+    evs = [[torch.cuda.Event(enable_timing=True) for _ in range(len(STEPS) + 1)] for _ in range(args.steps)]
+    start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    torch.cuda.synchronize()
+    start.record()
+    for i in range(args.steps):
+        run(sets[i % nsets], evs[i])
+    end.record()
+    sclk_eager = read_sclk_mhz()
+    torch.cuda.synchronize()
+    ms_step = eager_ms_step = start.elapsed_time(end) / args.steps
+    dur = np.array([[e[j].elapsed_time(e[j + 1]) for j in range(len(STEPS))] for e in evs]).mean(axis=0)
+    if not args.no_graph:
+        ms_step = time_graph(torch, lambda i: run(sets[i % nsets]), args.steps)
+    att_us = round(float(dur[3]) * 1e3, 3)
+    if not args.no_graph:
+        att_us = round(time_graph(torch, lambda i: attention(sets[i % nsets]), args.steps) * 1e3, 3)
+    att_ops = 4.0 * M * M * C
+    ops = att_ops + 12.0 * C * C + sum(2.0 * M * L["N"] * L["K"] + 2.0 * M * L["r"] * (L["K"] + L["N"]) for L in layers)
+    achieved = att_ops / (att_us * 1e-6) / 1e12
+    print(json.dumps({
+        "metric": f"whole DiT block (width {C}, {heads} heads, {'MXFP4' if mx else 'W4A4'} linears) TOPS and tokens/s at M={M}",
+        "value": round(ops / (ms_step * 1e-3) / 1e12, 2),
+        "unit": "TOPS",
+        "n_gpus": 1,
+        "steps": args.steps,
+        "warmup": args.warmup,
+        "ms_per_step": round(ms_step, 5),
+        "higher_is_better": True,
+        "scaling": "weak",
+        "vs_baseline": None,
+        "dtype": f"{'mxfp4' if mx else 'int4'} linears, bf16 attention, norms and modulation",
+        "data": "synthetic",
+        "config": {"workload": "dit_block_full", "format": args.format, "M": M, "width": C, "heads": heads,
+                   "rank": layers[0]["r"], "rotated_sets": nsets, "hip_graph": not args.no_graph},
+        "eager_ms_per_step": round(eager_ms_step, 5),
+        "tokens_per_s": round(M / (ms_step * 1e-3), 1),
+        "roofline": {"kernel": "attention", "bound": "mfma", "achieved": round(achieved, 2), "peak": PEAK_BF16_TFLOPS,
+                     "unit": "TFLOP/s", "frac": round(achieved / PEAK_BF16_TFLOPS, 4),
+                     "algorithmic": {"ops": att_ops, "bytes": 8 * M * C}, "traffic": None, "avg_launch_us": att_us},
+        "eager_us": {n: round(float(v) * 1e3, 2) for n, v in zip(STEPS, dur)},
+        "clock": {"settle_steps": settle_n, "settle_ms": round(settle_ms, 1), "sclk_mhz_eager": sclk_eager,
+                  "source": "pp_dpm_sclk (current DPM level)"},
+        "pack_s": round(pack_s, 2),
+    }), flush=True)
 
 
 def cpu_baseline_block(layers, seconds, mx):
