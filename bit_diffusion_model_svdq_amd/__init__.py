@@ -659,18 +659,21 @@ if _torch is not None:
     _T_I32 = (_torch.int32,)
 
 
-def _need_heads(t, name, head_dim=None, rows=None, heads=None):
-    """A [rows, heads, head_dim] bf16 tensor whose rows may lie apart (a column slice of a
-    projection's output); returns the row stride in elements."""
-    try:
-        device, dtype, shape, strides = t.device, t.dtype, t.shape, t.stride()
-        t.data_ptr
-    except AttributeError:
-        raise TypeError(f"{name} must be a torch tensor on the GPU") from None
-    if device.type != "cuda":
-        raise ValueError(f"{name} must live on the GPU (got device {device})")
-    if (_DTYPE_NAMES.get(dtype) or _dtype_name(t)) not in _BF16:
+def _need_bf16(t, name):
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must live on the GPU (got device {t.device})")
+    if _dtype_name(t) not in _BF16:
         raise ValueError(f"{name} must have dtype {' or '.join(_BF16)} (got {_dtype_name(t)})")
+
+
+def _need_heads(t, name, index=None, head_dim=None, rows=None, heads=None):
+    """A [rows, heads, head_dim] bf16 tensor on device `index` whose rows may lie apart (a column
+    slice of a projection's output); returns the row stride in elements."""
+    shape, strides, device = t.shape, t.stride(), t.get_device()
+    if device < 0 or t.dtype not in _T_BF16:
+        _need_bf16(t, name)
+    if index is not None and device != index:
+        raise ValueError(f"tensors live on different devices: {name} on {t.device}")
     if (len(shape) != 3 or (rows is not None and shape[0] != rows) or (heads is not None and shape[1] != heads)
             or (head_dim is not None and shape[2] != head_dim)):
         raise ValueError(f"{name} must have shape {(rows, heads, head_dim)} (got {tuple(shape)})")
@@ -679,6 +682,13 @@ def _need_heads(t, name, head_dim=None, rows=None, heads=None):
     if (d > 1 and inner != 1) or (h > 1 and between != d):
         raise ValueError(f"{name}: the heads of a row must be contiguous (strides {(ld, between, inner)})")
     return ld if n > 1 else h * d
+
+
+def _need_tensors(**ts):
+    """TypeError for the first operand that is neither a tensor nor None."""
+    for name, t in ts.items():
+        if not (t is None or hasattr(t, "data_ptr") and hasattr(t, "get_device")):
+            raise TypeError(f"{name} must be a torch tensor on the GPU")
 
 
 def _need_cu(cu, name, batch=None):
@@ -703,26 +713,30 @@ def svdq_attention_forward(Q, K, V, cu_q, cu_k, scale, causal, O, lse=None, work
     """O [Tq, Hq, D] (written) = attention of Q [Tq, Hq, D] over K, V [Tk, Hkv, D], bf16, for packed
     sequences with offsets cu_q, cu_k (int32 [batch + 1] on the GPU; None: one sequence).  Rows may lie
     apart (slices of a fused projection's output).  lse: float32 [Hq, Tq] or None."""
-    ldq = _need_heads(Q, "Q")
-    total_q, heads_q, d = Q.shape
-    ldk = _need_heads(K, "K", d)
-    total_k, heads_kv = K.shape[:2]
-    ldv = _need_heads(V, "V", d, total_k, heads_kv)
-    ldo = _need_heads(O, "O", d, total_q, heads_q)
-    batch = 1 if cu_q is None else cu_q.shape[0] - 1
-    index = Q.get_device()
-    if not (_agree(index, (cu_q, _T_I32, (batch + 1,)), (cu_k, _T_I32, (batch + 1,)), (lse, _T_F32, (heads_q, total_q)))
-            and K.get_device() == index and V.get_device() == index and O.get_device() == index and batch >= 1
-            and (batch == 1 or cu_k is not None) and (workspace is None or workspace.get_device() == index)):
-        batch = _need_cu(cu_q, "cu_q")
-        if (cu_q is None) != (cu_k is None) and batch > 1:
-            raise ValueError("cu_q and cu_k must both be given for more than one sequence")
-        if cu_k is not None:
-            _need_cu(cu_k, "cu_k", batch)
-        _need(lse, "lse", ("float32",), (heads_q, total_q), optional=True)
-        _same_device(Q, K, V, O, cu_q, cu_k, lse, workspace)
-    if workspace is not None and not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
+    try:
+        index = Q.get_device()
+        ldq = _need_heads(Q, "Q")
+        total_q, heads_q, d = Q.shape
+        ldk = _need_heads(K, "K", index, d)
+        total_k, heads_kv, _ = K.shape
+        ldv = _need_heads(V, "V", index, d, total_k, heads_kv)
+        ldo = _need_heads(O, "O", index, d, total_q, heads_q)
+        batch = 1 if cu_q is None else cu_q.shape[0] - 1
+        if not (_agree(index, (cu_q, _T_I32, (batch + 1,)), (cu_k, _T_I32, (batch + 1,)), (lse, _T_F32, (heads_q, total_q)))
+                and batch >= 1 and (batch == 1 or cu_k is not None)
+                and (workspace is None or workspace.get_device() == index)):
+            batch = _need_cu(cu_q, "cu_q")
+            if (cu_q is None) != (cu_k is None) and batch > 1:
+                raise ValueError("cu_q and cu_k must both be given for more than one sequence")
+            if cu_k is not None:
+                _need_cu(cu_k, "cu_k", batch)
+            _need(lse, "lse", ("float32",), (heads_q, total_q), optional=True)
+            _same_device(Q, K, V, O, cu_q, cu_k, lse, workspace)
+        if workspace is not None and not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+    except AttributeError:
+        _need_tensors(Q=Q, K=K, V=V, O=O, cu_q=cu_q, cu_k=cu_k, lse=lse, workspace=workspace)
+        raise
     _launch(index, stream, _lib.svdq_attention_forward, Q.data_ptr(), ldq, K.data_ptr(), ldk, V.data_ptr(), ldv,
             _ptr(cu_q), _ptr(cu_k), batch, total_q, total_k, heads_q, heads_kv, d, scale, int(causal), O.data_ptr(), ldo,
             _ptr(lse), _ptr(workspace), _bytes(workspace))
@@ -734,14 +748,9 @@ def _need_vectors(t, name, batch, width, index):
     the row stride."""
     if t is None:
         return 0
-    try:
-        device, shape, strides = t.get_device(), t.shape, t.stride()
-    except AttributeError:
-        raise TypeError(f"{name} must be a torch tensor on the GPU") from None
-    if t.device.type != "cuda":
-        raise ValueError(f"{name} must live on the GPU (got device {t.device})")
-    if (_DTYPE_NAMES.get(t.dtype) or _dtype_name(t)) not in _BF16:
-        raise ValueError(f"{name} must have dtype {' or '.join(_BF16)} (got {_dtype_name(t)})")
+    device, shape, strides = t.get_device(), t.shape, t.stride()
+    if device < 0 or t.dtype not in _T_BF16:
+        _need_bf16(t, name)
     if shape != (batch, width):
         raise ValueError(f"{name} must have shape {(batch, width)} (got {tuple(shape)})")
     if device != index:
@@ -758,27 +767,32 @@ def svdq_block_norm_forward(x, y, cu, post, post_weight, gate, residual_scale, b
     SVDQ_NORM_*.  x and x_out float32 or bf16, everything else bf16; gate, scale, shift [batch, width]
     (rows may lie apart).  cu: int32 [batch + 1] offsets of the packed sequences, None for one sequence.
     Absent operands are None; x_out may be x and h may be y."""
-    if x.dim() != 2:
-        raise ValueError("x must be a [rows, width] tensor")
-    rows, width = shape = x.shape
-    batch = 1 if cu is None else cu.shape[0] - 1
-    index = x.get_device()
-    f32 = _dtype_name(x) == "float32"
-    stream_types = _T_F32 if f32 else _T_BF16
-    if not (_agree(index, (x, stream_types, shape), (y, _T_BF16, shape), (x_out, stream_types, shape), (h, _T_BF16, shape),
-                   (cu, _T_I32, (batch + 1,)), (post_weight, _T_BF16, (width,)), (pre_weight, _T_BF16, (width,)),
-                   (pre_bias, _T_BF16, (width,))) and batch >= 1):
-        _need(x, "x", _BF16_F32)
-        _need(x_out, "x_out", ("float32",) if f32 else _BF16, (rows, width), optional=True)
-        _need(y, "y", _BF16, (rows, width), optional=True)
-        _need(h, "h", _BF16, (rows, width), optional=True)
-        batch = _need_cu(cu, "cu")
-        for t, name in ((post_weight, "post_weight"), (pre_weight, "pre_weight"), (pre_bias, "pre_bias")):
-            _need(t, name, _BF16, (width,), optional=True)
-        _same_device(x, y, cu, post_weight, pre_weight, pre_bias, x_out, h)
-    ld_gate = _need_vectors(gate, "gate", batch, width, index)
-    ld_scale = _need_vectors(scale, "scale", batch, width, index)
-    ld_shift = _need_vectors(shift, "shift", batch, width, index)
+    try:
+        if x.dim() != 2:
+            raise ValueError("x must be a [rows, width] tensor")
+        rows, width = shape = x.shape
+        batch = 1 if cu is None else cu.shape[0] - 1
+        index = x.get_device()
+        f32 = _dtype_name(x) == "float32"
+        stream_types = _T_F32 if f32 else _T_BF16
+        if not (_agree(index, (x, stream_types, shape), (y, _T_BF16, shape), (x_out, stream_types, shape), (h, _T_BF16, shape),
+                       (cu, _T_I32, (batch + 1,)), (post_weight, _T_BF16, (width,)), (pre_weight, _T_BF16, (width,)),
+                       (pre_bias, _T_BF16, (width,))) and batch >= 1):
+            _need(x, "x", _BF16_F32)
+            _need(x_out, "x_out", ("float32",) if f32 else _BF16, (rows, width), optional=True)
+            _need(y, "y", _BF16, (rows, width), optional=True)
+            _need(h, "h", _BF16, (rows, width), optional=True)
+            batch = _need_cu(cu, "cu")
+            for t, name in ((post_weight, "post_weight"), (pre_weight, "pre_weight"), (pre_bias, "pre_bias")):
+                _need(t, name, _BF16, (width,), optional=True)
+            _same_device(x, y, cu, post_weight, pre_weight, pre_bias, x_out, h)
+        ld_gate = _need_vectors(gate, "gate", batch, width, index)
+        ld_scale = _need_vectors(scale, "scale", batch, width, index)
+        ld_shift = _need_vectors(shift, "shift", batch, width, index)
+    except AttributeError:
+        _need_tensors(x=x, y=y, cu=cu, post_weight=post_weight, gate=gate, pre_weight=pre_weight, pre_bias=pre_bias,
+                      scale=scale, shift=shift, x_out=x_out, h=h)
+        raise
     _launch(index, stream, _lib.svdq_block_norm_forward, x.data_ptr(), SVDQ_F32 if f32 else SVDQ_BF16, _ptr(y), rows,
             width, _ptr(cu), batch, post, _ptr(post_weight), _ptr(gate), ld_gate, residual_scale, branch_scale, pre,
             _ptr(pre_weight), _ptr(pre_bias), _ptr(scale), ld_scale, _ptr(shift), ld_shift, eps, _ptr(x_out), _ptr(h))
@@ -792,23 +806,27 @@ def svdq_linear_bf16_workspace_bytes(M: int, K: int, N: int) -> int:
 def svdq_linear_bf16_forward(X, W, bias, activation, residual, Y, workspace=None, stream=None):
     """Y [M, N] (written) = act(X W^T + bias) + residual; X [M, K], W [N, K], bias [N] bf16, Y and
     residual bf16 or float32 alike (residual may be Y)."""
-    if X.dim() != 2 or W.dim() != 2:
-        raise ValueError("X must be a [M, K] and W a [N, K] tensor")
-    M, K = X.shape
-    N = W.shape[0]
-    index = X.get_device()
-    f32 = _dtype_name(Y) == "float32"
-    out_types = _T_F32 if f32 else _T_BF16
-    if not (_agree(index, (X, _T_BF16, (M, K)), (W, _T_BF16, (N, K)), (bias, _T_BF16, (N,)), (Y, out_types, (M, N)),
-                   (residual, out_types, (M, N))) and (workspace is None or workspace.get_device() == index)):
-        _need(X, "X", _BF16)
-        _need(W, "W", _BF16, (N, K))
-        _need(bias, "bias", _BF16, (N,), optional=True)
-        _need(Y, "Y", _BF16_F32, (M, N))
-        _need(residual, "residual", ("float32",) if f32 else _BF16, (M, N), optional=True)
-        _same_device(X, W, bias, residual, Y, workspace)
-    if workspace is not None and not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
+    try:
+        if X.dim() != 2 or W.dim() != 2:
+            raise ValueError("X must be a [M, K] and W a [N, K] tensor")
+        M, K = X.shape
+        N = W.shape[0]
+        index = X.get_device()
+        f32 = _dtype_name(Y) == "float32"
+        out_types = _T_F32 if f32 else _T_BF16
+        if not (_agree(index, (X, _T_BF16, (M, K)), (W, _T_BF16, (N, K)), (bias, _T_BF16, (N,)), (Y, out_types, (M, N)),
+                       (residual, out_types, (M, N))) and (workspace is None or workspace.get_device() == index)):
+            _need(X, "X", _BF16)
+            _need(W, "W", _BF16, (N, K))
+            _need(bias, "bias", _BF16, (N,), optional=True)
+            _need(Y, "Y", _BF16_F32, (M, N))
+            _need(residual, "residual", ("float32",) if f32 else _BF16, (M, N), optional=True)
+            _same_device(X, W, bias, residual, Y, workspace)
+        if workspace is not None and not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+    except AttributeError:
+        _need_tensors(X=X, W=W, bias=bias, residual=residual, Y=Y, workspace=workspace)
+        raise
     _launch(index, stream, _lib.svdq_linear_bf16_forward, X.data_ptr(), M, K, N, W.data_ptr(), _ptr(bias),
             int(activation), _ptr(residual), Y.data_ptr(), SVDQ_F32 if f32 else SVDQ_BF16, _ptr(workspace),
             _bytes(workspace))

@@ -167,6 +167,7 @@ __device__ inline bool find_tile(const Params& p, int rows, int t, int lane, Pla
       return true;
     }
     t -= __builtin_amdgcn_readlane(end, 63);
+    if (t < 0) return false;      // offsets that overlap so often that the count wrapped
   }
   return false;
 }

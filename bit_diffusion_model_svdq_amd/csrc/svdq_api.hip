@@ -535,8 +535,8 @@ svdq_status svdq_attention_forward(const uint16_t* Q, int64_t ldq, const uint16_
                                    void* workspace, size_t workspace_bytes, void* stream) {
   return guarded([&]() -> svdq_status {
     SVDQ_TRY(check_attention_shape(batch, total_q, total_k, heads_q, heads_kv, head_dim));
-    if (!(scale > 0.f) || !isfinite(scale))
-      return fail(SVDQ_ERR_INVALID_ARG, "scale must be positive and finite (got %g)", (double)scale);
+    if (!(scale > 0.f) || scale > 0x1p126f)      // the kernels take scale log2(e)
+      return fail(SVDQ_ERR_INVALID_ARG, "scale must be positive and at most 2^126 (got %g)", (double)scale);
     if (causal != 0 && causal != 1) return fail(SVDQ_ERR_INVALID_ARG, "causal must be 0 or 1 (got %d)", causal);
     if (batch > 1 && (!cu_q || !cu_k))
       return fail(SVDQ_ERR_INVALID_ARG, "cu_q and cu_k must not be NULL for batch=%d", batch);

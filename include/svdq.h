@@ -367,7 +367,9 @@ svdq_status svdq_quantize_activations_mxfp4(const uint16_t* X, int M, int K, con
  * What a transformer block of a 4-bit diffusion model runs between its
  * SVDQuant linears: attention, the norms with their modulation, gate and
  * residual, and the linears that stay in 16 bits.  All of them take device
- * memory, run asynchronously on `stream` and allocate nothing.
+ * memory, run asynchronously on `stream` and allocate nothing.  Calls that may
+ * run at the same time (on different streams) need workspaces of their own;
+ * calls that follow each other may share one, whatever it holds.
  *
  * Packed sequences: `batch` sequences of different lengths lie behind each
  * other in one tensor of rows.  cu [batch + 1] (int32, device memory) holds
@@ -401,7 +403,7 @@ size_t svdq_attention_workspace_bytes(int64_t total_q, int64_t total_k, int batc
  * lse (float32 [heads_q, total_q], may be NULL): ln sum_j exp(scale Q . K).
  * Requires head_dim a multiple of 8 up to 128 and ldk, ldv up to 2^24 (above:
  * SVDQ_ERR_UNSUPPORTED),
- * heads_q a multiple of heads_kv, scale positive and finite.  Non-finite K or
+ * heads_q a multiple of heads_kv, scale positive and at most 2^126.  Non-finite K or
  * V elements can reach every query of their sequence and key head, also the
  * queries that the causal mask hides them from, but no other sequence.
  * The sums run in an order that depends on the shapes only, so equal calls
@@ -453,8 +455,9 @@ size_t svdq_linear_bf16_workspace_bytes(int64_t M, int K, int N);
  * projection): Y = act(X W^T + bias) + residual, X [M, K], W [N, K], bias [N]
  * bf16, sums in float32, one rounding.  Y and residual [M, N] have type
  * `out_dtype` (an svdq_dtype); bias and residual may be NULL, and residual may
- * be Y.  `activation` is any svdq_activation.  K a multiple of 8; any M >= 0
- * (M = 0 does nothing) and N >= 1. */
+ * be Y; otherwise Y must not overlap the inputs.  `activation` is any
+ * svdq_activation.  K a multiple of 8; any M >= 0 (M = 0 does nothing) and
+ * N >= 1. */
 svdq_status svdq_linear_bf16_forward(const uint16_t* X, int64_t M, int K, int N, const uint16_t* W,
                                      const uint16_t* bias, int activation, const void* residual,
                                      void* Y, int out_dtype, void* workspace,

@@ -31,7 +31,7 @@ def attention(**over):
     (dict(heads_q=1), INVALID), (dict(head_dim=0), INVALID), (dict(head_dim=60), INVALID),
     (dict(head_dim=136, ldq=2048, ldk=512, ldv=512, ldo=2048), UNSUPPORTED),
     (dict(scale=0.0), INVALID), (dict(scale=-1.0), INVALID), (dict(scale=float("inf")), INVALID),
-    (dict(scale=float("nan")), INVALID), (dict(causal=2), INVALID),
+    (dict(scale=float("nan")), INVALID), (dict(scale=2.0**127), INVALID), (dict(causal=2), INVALID),
     (dict(ldq=504), INVALID), (dict(ldq=516), INVALID), (dict(ldk=120), INVALID), (dict(ldv=129), INVALID),
     (dict(ldo=256), INVALID), (dict(ldk=(1 << 24) + 8), UNSUPPORTED), (dict(ldv=1 << 30), UNSUPPORTED),
     (dict(Q=None), INVALID), (dict(K=None), INVALID), (dict(V=None), INVALID), (dict(O=None), INVALID),
@@ -210,6 +210,28 @@ def test_linear_binding_checks(over, err):
     a.update(over)
     with pytest.raises(ValueError, match=err):
         S.svdq_linear_bf16_forward(*a.values())
+
+
+def test_operands_that_are_no_tensors_are_named():
+    bf = torch.bfloat16
+    q, x, cu = heads(10, 4, 64), g((10, 64), bf), [0, 10]
+    with pytest.raises(TypeError, match="cu_q must be a torch tensor"):
+        S.svdq_attention_forward(q, q, q, cu, cu, 0.125, False, q)
+    with pytest.raises(TypeError, match="Q must be a torch tensor"):
+        S.svdq_attention_forward(np.zeros((10, 4, 64)), q, q, None, None, 0.125, False, q)
+    with pytest.raises(TypeError, match="workspace must be a torch tensor"):
+        S.svdq_attention_forward(q, q, q, None, None, 0.125, False, q, None, 1 << 20)
+    for over, name in ((dict(x=1.0), "x"), (dict(cu=cu), "cu"), (dict(gate=1.0), "gate"), (dict(h=np.zeros((10, 64))), "h")):
+        a = dict(x=x, y=x, cu=None, post=0, w=None, gate=None, rs=1.0, bs=1.0, pre=2, pw=None, pb=None, scale=None,
+                 shift=None, eps=1e-6, x_out=x, h=x)
+        a.update(over)
+        with pytest.raises(TypeError, match=f"{name} must be a torch tensor"):
+            S.svdq_block_norm_forward(*a.values())
+    for i, name in ((0, "X"), (2, "bias"), (5, "Y")):
+        a = [x, g((16, 64), bf), None, 0, None, g((10, 16), bf)]
+        a[i] = np.zeros((10, 64))
+        with pytest.raises(TypeError, match=f"{name} must be a torch tensor"):
+            S.svdq_linear_bf16_forward(*a)
 
 
 # ------------------------------------------------------------------ oracles against torch
