@@ -77,24 +77,35 @@ __device__ inline f32x4 bias4(const LinearArgs& a, int n) {
   return v;
 }
 
-// Four neighbouring outputs n .. n + 3 of row m in float32: bias, activation and
-// residual (of elements inside the matrix; the others are anything).
-template <class O, int ACT>
-__device__ inline f32x4 value4(f32x4 v, f32x4 bias, const LinearArgs& a, int64_t m, int n) {
+// The residual at n .. n + 3 of row m as it lies in memory; zeros outside the
+// matrix and where there is none.
+__device__ inline f32x4 residual4(const LinearArgs& a, int64_t m, int n, float) {
+  f32x4 v = f32x4{0.f, 0.f, 0.f, 0.f};
+  if (!a.residual || m >= a.M || n >= a.N) return v;
+  const float* r = static_cast<const float*>(a.residual) + m * a.N + n;
+  if (n + 4 <= a.N) return *reinterpret_cast<const f32x4u*>(r);
+  for (int i = 0; i < 4; ++i)
+    if (n + i < a.N) v[i] = r[i];
+  return v;
+}
+__device__ inline u32x2 residual4(const LinearArgs& a, int64_t m, int n, uint16_t) {
+  u32x2 v = u32x2{0u, 0u};
+  if (!a.residual || m >= a.M || n >= a.N) return v;
+  const uint16_t* r = static_cast<const uint16_t*>(a.residual) + m * a.N + n;
+  if (n + 4 <= a.N) return *reinterpret_cast<const u32x2u*>(r);
+  for (int i = 0; i < 4; ++i)
+    if (n + i < a.N) v[i >> 1] |= (uint32_t)r[i] << (16 * (i & 1));
+  return v;
+}
+__device__ inline f32x4 widen(f32x4 v) { return v; }
+__device__ inline f32x4 widen(u32x2 v) { return unpack4(v); }
+
+// Four neighbouring outputs in float32 but for the residual.
+template <int ACT>
+__device__ inline f32x4 value4(f32x4 v, f32x4 bias) {
   v += bias;
 #pragma unroll
   for (int i = 0; i < 4; ++i) v[i] = activate<ACT>(v[i]);
-  if (!a.residual || m >= a.M || n >= a.N) return v;
-  const O* r = static_cast<const O*>(a.residual) + m * a.N + n;
-  if constexpr (sizeof(O) == 4) {
-    if (n + 4 <= a.N) return v + *reinterpret_cast<const f32x4u*>(r);
-    for (int i = 0; i < 4; ++i)
-      if (n + i < a.N) v[i] += r[i];
-  } else {
-    if (n + 4 <= a.N) return v + unpack4(*reinterpret_cast<const u32x2u*>(r));
-    for (int i = 0; i < 4; ++i)
-      if (n + i < a.N) v[i] += bf16_value(r[i]);
-  }
   return v;
 }
 
@@ -130,7 +141,7 @@ __device__ inline void store4(f32x4 v, const LinearArgs& a, int64_t m, int n) {
 
 template <class O, int ACT>
 __device__ inline void finish4(f32x4 v, f32x4 bias, const LinearArgs& a, int64_t m, int n) {
-  store4<O>(value4<O, ACT>(v, bias, a, m, n), a, m, n);
+  store4<O>(value4<ACT>(v, bias) + widen(residual4(a, m, n, O())), a, m, n);
 }
 
 constexpr int KS = 64;            // channels per step: two MFMAs deep
@@ -246,14 +257,21 @@ struct Wave {
         acc[tm][tn] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[tn], xf[tm], acc[tm][tn], 0, 0, 0);
   }
 
+  // The residual of register quad (tm, tn).
+  template <class O>
+  __device__ auto residual(const LinearArgs& a, int tm, int tn) const {
+    return residual4(a, (int64_t)m0 + wm * C::TM * 16 + 16 * tm + fr, n0 + wn * C::TN * 16 + 16 * tn + 4 * fk, O());
+  }
+
   // The wave's outputs.  float32 goes straight from the accumulators (64
   // neighbouring bytes of a row per instruction); bf16 through the wave's own
   // staging rows, 16 rows at a time, so that whole lines are stored, which then
   // stream out non-temporally: 4608 x 3072 -> 12288 300 us, against 306 with
   // stores that allocate in the caches and 330 with 8-byte stores straight from
   // the accumulators.
-  template <class O, int ACT>
-  __device__ void outputs(const LinearArgs& a, uint8_t* stage) {
+  // add(v, tm, tn): v and the residual of a register quad.
+  template <class O, int ACT, class F>
+  __device__ void outputs(const LinearArgs& a, uint8_t* stage, F add) {
     const int n1 = n0 + wn * C::TN * 16;
     const int64_t m1 = (int64_t)m0 + wm * C::TM * 16;
     f32x4 bias[C::TN];
@@ -264,7 +282,7 @@ struct Wave {
       for (int tm = 0; tm < C::TM; ++tm)
 #pragma unroll
         for (int tn = 0; tn < C::TN; ++tn)
-          finish4<O, ACT>(acc[tm][tn], bias[tn], a, m1 + 16 * tm + fr, n1 + 16 * tn + 4 * fk);
+          store4<O>(add(value4<ACT>(acc[tm][tn], bias[tn]), tm, tn), a, m1 + 16 * tm + fr, n1 + 16 * tn + 4 * fk);
     } else {
       uint16_t* rows = reinterpret_cast<uint16_t*>(stage) + wave * 16 * C::PITCH;
       constexpr int CPR = 2 * C::TN;      // 16-byte chunks of a row
@@ -272,7 +290,7 @@ struct Wave {
       for (int tm = 0; tm < C::TM; ++tm) {
 #pragma unroll
         for (int tn = 0; tn < C::TN; ++tn) {
-          const f32x4 v = value4<O, ACT>(acc[tm][tn], bias[tn], a, m1 + 16 * tm + fr, n1 + 16 * tn + 4 * fk);
+          const f32x4 v = add(value4<ACT>(acc[tm][tn], bias[tn]), tm, tn);
           *reinterpret_cast<u32x2*>(rows + fr * C::PITCH + 16 * tn + 4 * fk) = pack4(v);
         }
         // a wave's LDS accesses complete in issue order; the fences keep the
@@ -356,6 +374,16 @@ __global__ __launch_bounds__(C::THREADS, 2) void linear_tile(const LinearArgs a)
       w.multiply(xf, wf);
     }
   };
+  // small tiles have registers to spare for the residual, which then arrives
+  // beside the first copies
+  constexpr bool kEarly = !SHARES && C::TM * C::TN <= 8;
+  decltype(residual4(a, 0, 0, O())) early[kEarly ? C::TM : 1][kEarly ? C::TN : 1];
+  if constexpr (kEarly) {
+#pragma unroll
+    for (int tm = 0; tm < C::TM; ++tm)
+#pragma unroll
+      for (int tn = 0; tn < C::TN; ++tn) early[tm][tn] = w.template residual<O>(a, tm, tn);
+  }
   w.copy(sb, ring0);
   if constexpr (C::NR > 2) w.copy(sb + min(1, nsteps - 1), ring1);
   // whole turns of the ring without branches, then the rest
@@ -380,7 +408,12 @@ __global__ __launch_bounds__(C::THREADS, 2) void linear_tile(const LinearArgs a)
   if constexpr (SHARES)
     w.sums(a, share);
   else
-    w.template outputs<O, ACT>(a, stage);
+    w.template outputs<O, ACT>(a, stage, [&](f32x4 v, int tm, int tn) {
+      if constexpr (kEarly)
+        return v + widen(early[tm][tn]);
+      else
+        return a.residual ? v + widen(w.template residual<O>(a, tm, tn)) : v;
+    });
 }
 
 // The 256 x 256 tile: waves 0..3 and 4..7, one of each on every SIMD, are half a
@@ -442,7 +475,9 @@ __global__ __launch_bounds__(Big::THREADS, 2) void linear_turns(const LinearArgs
   }
   if (j < nsteps) step(j, ring0, ring1);
   if (!second) barrier();
-  w.template outputs<O, ACT>(a, stage);
+  w.template outputs<O, ACT>(a, stage, [&](f32x4 v, int tm, int tn) {
+    return a.residual ? v + widen(w.template residual<O>(a, tm, tn)) : v;
+  });
 }
 
 // Sums the shares in order and finishes the outputs, four per thread.
