@@ -24,10 +24,10 @@
 //                 wave streams its share of the channels of 16 weight rows
 //                 straight into registers.
 //
-// Measured: 4608 x 3072 -> 12288 300 us (1160 TFLOP/s) with 256 x 256 turns; with
-// bf16 stored straight from the accumulators 330 us, 347 with the same tile in
-// one group, 357 / 442 / 501 with the smaller tiles; 1155 x 1288 -> 1290 16.2 us with 128 x 64, 16.8 with 64 x 64, 27 with 128 x 128;
-// 2 x 3072 -> 18432 23.7 us (4.8 TB/s) in linear_rows.
+// Measured: 4608 x 3072 -> 12288 300 us (1160 TFLOP/s) with 256 x 256 turns (with bf16
+// stored straight from the accumulators 330 us), 354 / 444 / 502 with the smaller
+// tiles; 1155 x 1288 -> 1290 with a float32 residual 14.2 us with 128 x 64, 15.9 with
+// 64 x 64, 27 with 128 x 128; 2 x 3072 -> 18432 23.7 us (4.8 TB/s) in linear_rows.
 #include <algorithm>
 
 #include "gemm_tail.h"
@@ -168,6 +168,7 @@ struct Tile {
 using Big = Tile<2, 4, 8, 4, 2>;     // 256 x 256, 8 waves, 128 KB: linear_turns
 using Med = Tile<2, 2, 4, 4, 2>;     // 128 x 128, 4 waves, 64 KB
 using Tall = Tile<2, 2, 4, 2, 3>;    // 128 x 64, 4 waves, 72 KB
+using Deep = Tile<2, 2, 2, 2, 3>;    //  64 x 64, 4 waves, 48 KB: one step more in flight
 using Small = Tile<2, 2, 2, 2, 2>;   //  64 x 64, 4 waves, 32 KB
 
 // XOR key of the 16-byte chunks of an LDS row: a fragment read covers 16
@@ -539,7 +540,7 @@ __global__ __launch_bounds__(kRowWaves * 64) void linear_rows(const LinearArgs a
   finish4<O, ACT>(v, bias4(a, n0 + 4 * fk), a, fr, n0 + 4 * fk);
 }
 
-enum Kind { kKindRows, kKindBig, kKindMed, kKindTall, kKindSmall };
+enum Kind { kKindRows, kKindBig, kKindMed, kKindTall, kKindDeep, kKindSmall };
 struct Plan {
   Kind kind = kKindRows;
   int splits = 1;
@@ -555,12 +556,15 @@ int64_t tiles_of(int64_t M, int64_t N) {
 // Tile and shares by an estimate of the time, in us: a CU that gets n tiles
 // takes max(alone, n each) for a step of 64 channels of all of them (`alone`:
 // what the copies' latency costs one tile; `each`: its part of the CU's
-// bandwidth; 128 x 128 tiles run in pairs, so an odd one costs two), and shares
-// cost a second launch and the traffic of their sums.  Measured for a step:
-// 256 x 256 1.6 alone, 1.7 each; 128 x 128 0.8 / 0.5; 128 x 64 0.31 / 0.33 (and 0.8
-// more to fill its ring); 64 x 64 0.36 / 0.19.  On 17 shapes from 925 x 440 -> 89
-// to 4608 x 12288 -> 3072 the choice is the fastest or within 10 % of it, where
-// always taking 128 x 64 loses up to 57 % and always 64 x 64 up to 96 %.
+// bandwidth; 128 x 128 tiles run in pairs, so an odd one costs two), `fill` once
+// for filling the ring and storing the tile, and shares cost a second launch
+// and the traffic of their sums.  The table's figures are measured ones.  64 x 64
+// tiles come in two forms: with two steps of copies in flight while a CU has two
+// of them at most (512 x 1280 -> 1280 8.0 us, 11.5 with one step; 32 x 3072 -> 18432
+// 30.9 and 39.2), else with one, since more of the smaller workgroups fit a CU
+// (4096 x 640 -> 640 9.1 us, 10.8 with two steps).  Over 29 shapes from 77 x 640 -> 640
+// to 4608 x 12288 -> 3072 the choice is the fastest or within 10 % of it, where always
+// taking 128 x 64 loses up to 61 % and always 64 x 64 up to 83 %.
 constexpr int kMaxSplits = 8;
 constexpr int kMinShareSteps = 8;          // below that a share is all latency
 constexpr size_t kMaxPartBytes = size_t(32) << 20;
@@ -575,15 +579,17 @@ Plan plan_of(int M, int K, int N) {
     Kind kind;
     int64_t tiles;
     double alone, each, fill;
-  } tile[] = {{kKindBig, tiles_of<Big>(M, N), 1.6, 1.7, 0.0},
-              {kKindMed, tiles_of<Med>(M, N), 0.8, 0.5, 0.0},
-              {kKindTall, tiles_of<Tall>(M, N), 0.31, 0.33, 0.8},
-              {kKindSmall, tiles_of<Small>(M, N), 0.36, 0.19, 0.0}};
+  } tile[] = {{kKindBig, tiles_of<Big>(M, N), 1.4, 1.5, 3.5},
+              {kKindMed, tiles_of<Med>(M, N), 0.8, 0.47, 0.0},
+              {kKindTall, tiles_of<Tall>(M, N), 0.31, 0.36, 0.8},
+              {kKindDeep, tiles_of<Deep>(M, N), 0.26, 0.28, 0.0},
+              {kKindSmall, tiles_of<Small>(M, N), 0.42, 0.24, 0.0}};
   const int cus = device_cu_count();
   const int64_t steps = ((int64_t)K + KS - 1) / KS;
   double least = 0;
   for (const auto& t : tile)
-    for (int s = 1; s <= (t.kind == kKindBig ? 1 : kMaxSplits); s *= 2) {
+    for (int s = 1; s <= (t.kind == kKindBig || t.kind == kKindSmall ? 1 : kMaxSplits); s *= 2) {
+      if ((t.kind == kKindDeep && t.tiles * s > 2 * cus) || (t.kind == kKindSmall && t.tiles <= 2 * cus)) break;
       const size_t part = s > 1 ? (size_t)s * M * (((size_t)N + 3) / 4 * 4) * sizeof(float) : 0;
       if (s > 1 && (steps / s < kMinShareSteps || part > kMaxPartBytes)) break;
       int64_t n = (t.tiles * s + cus - 1) / cus;
@@ -602,12 +608,15 @@ Plan plan_of(int M, int K, int N) {
 }
 
 template <class C, class O, int ACT>
+hipError_t launch_whole(const Plan& p, const LinearArgs& a, hipStream_t stream) {
+  hipLaunchKernelGGL((linear_tile<C, O, ACT, false>), dim3((unsigned)p.blocks), dim3(C::THREADS), 0, stream, a);
+  return hipGetLastError();
+}
+
+template <class C, class O, int ACT>
 hipError_t launch_tile(const Plan& p, const LinearArgs& a, hipStream_t stream) {
+  if (p.splits == 1) return launch_whole<C, O, ACT>(p, a, stream);
   const dim3 grid((unsigned)p.blocks);
-  if (p.splits == 1) {
-    hipLaunchKernelGGL((linear_tile<C, O, ACT, false>), grid, dim3(C::THREADS), 0, stream, a);
-    return hipGetLastError();
-  }
   // the shares do not depend on the output's type or the activation
   hipLaunchKernelGGL((linear_tile<C, float, kActNone, true>), grid, dim3(C::THREADS), 0, stream, a);
   const hipError_t e = hipGetLastError();
@@ -631,8 +640,10 @@ hipError_t launch(const Plan& p, const LinearArgs& a, hipStream_t stream) {
       return launch_tile<Med, O, ACT>(p, a, stream);
     case kKindTall:
       return launch_tile<Tall, O, ACT>(p, a, stream);
+    case kKindDeep:
+      return launch_tile<Deep, O, ACT>(p, a, stream);
     case kKindSmall:
-      return launch_tile<Small, O, ACT>(p, a, stream);
+      return launch_whole<Small, O, ACT>(p, a, stream);
   }
   return hipErrorInvalidValue;
 }

@@ -69,7 +69,10 @@ def test_few_rows(M, K, N):
     (65, 8, 1), (65, 64, 15), (129, 40, 130), (200, 1024, 64), (333, 1160, 1003),     # 64 x 64 tiles, shares
     (1155, 1288, 1290), (128, 4096, 640), (70, 5000, 6),
     (2048, 200, 2100), (2100, 32, 2052),                                               # 128 x 128
-    (4100, 72, 4096), (4608, 136, 3850), (4096, 24, 4099),                             # 256 x 256
+    (4100, 72, 4096), (4608, 136, 3850), (4096, 24, 4099),
+    (4100, 72, 643), (9000, 64, 300), (2500, 520, 1101),                               # 64 x 64, many
+    (1155, 520, 1290), (2000, 968, 514),                                               # 128 x 64
+    (2050, 808, 4099), (2305, 712, 3833),                                              # 256 x 256
 ])
 @pytest.mark.parametrize("fp32", [False, True])
 def test_tiles(M, K, N, fp32):
@@ -77,7 +80,8 @@ def test_tiles(M, K, N, fp32):
 
 
 @pytest.mark.parametrize("act", ["none", "gelu", "silu"])
-@pytest.mark.parametrize("M,K,N", [(2, 512, 96), (100, 768, 72), (300, 64, 60), (2050, 96, 2080), (4352, 64, 4096)])
+@pytest.mark.parametrize("M,K,N", [(2, 512, 96), (100, 768, 72), (300, 64, 60), (2050, 96, 2080), (4352, 64, 4096),
+                                   (4100, 72, 643), (1155, 520, 1290), (2000, 808, 4100)])
 @pytest.mark.parametrize("bias,residual,fp32", [(True, False, False), (False, True, True), (True, True, False),
                                                 (False, False, True)])
 def test_epilogues(act, M, K, N, bias, residual, fp32):
