@@ -36,7 +36,6 @@
 // rounding of p to bf16 is relative.  p is rounded to bf16 because V is bf16
 // and the MFMA takes both operands in one type; l sums the unrounded values.
 #include <algorithm>
-#include <type_traits>
 
 #include "svdq_internal.h"
 
@@ -684,7 +683,7 @@ __global__ __launch_bounds__(NW * 64, 2) void attention_keys(const Params p) {
 
 // Joins the shares of a tile's rows: weights 2^(lse_s - max), rows summed in
 // share order in float32.  One wave per row: lane s holds share s's weight (at
-// most 64 shares), then each lane two channels, eight shares' loads at a time.
+// most 64 shares), then each lane two channels, eight shares at a time.
 __global__ __launch_bounds__(256) void attention_join(const Params p, int rows_per_tile) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -704,7 +703,17 @@ __global__ __launch_bounds__(256) void attention_join(const Params p, int rows_p
   const int token = row / p.group;
   const int head = hk * p.group + (row - token * p.group);
   auto slot = [&](int s) { return (((int64_t)s * p.tiles + tile) * p.heads_kv + hk) * rows_per_tile + r; };
+  const int d = 2 * lane;
+  const bool on = d < p.head_dim;
+  // eight shares at a time; past the last one the last again, with weight 0
+  float2 v[8];
+  auto load = [&](int s0) {
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      v[u] = *reinterpret_cast<const float2*>(p.part + slot(min(s0 + u, shares - 1)) * p.head_dim + (on ? d : 0));
+  };
   const float e = lane < shares ? p.part_lse[slot(lane)] : -INFINITY;
+  load(0);                                               // beside the weights' loads
   float top = e;
 #pragma unroll
   for (int s = 32; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor(top, s));
@@ -712,28 +721,18 @@ __global__ __launch_bounds__(256) void attention_join(const Params p, int rows_p
   float sum = weight;
 #pragma unroll
   for (int s = 32; s > 0; s >>= 1) sum += __shfl_xor(sum, s);
-  const int d = 2 * lane;
-  const bool on = d < p.head_dim;
   float a0 = 0.f, a1 = 0.f;
-  auto add = [&](auto count, int s0) {
-    constexpr int N = decltype(count)::value;
-    float2 v[N];
+  for (int s0 = 0; s0 < shares; s0 += 8) {
+    if (s0 > 0) load(s0);
 #pragma unroll
-    for (int u = 0; u < N; ++u)
-      v[u] = *reinterpret_cast<const float2*>(p.part + slot(s0 + u) * p.head_dim + (on ? d : 0));
-#pragma unroll
-    for (int u = 0; u < N; ++u) {
-      const float w = __shfl(weight, s0 + u);
-      if (w > 0.f) {                                     // a share without weight has written nothing
+    for (int u = 0; u < 8; ++u) {
+      const float w = __shfl(weight, (s0 + u) & 63);
+      if (s0 + u < shares && w > 0.f) {                  // a share without weight has written nothing
         a0 = __builtin_fmaf(w, v[u].x, a0);
         a1 = __builtin_fmaf(w, v[u].y, a1);
       }
     }
-  };
-  int s0 = 0;
-  for (; s0 + 8 <= shares; s0 += 8) add(std::integral_constant<int, 8>{}, s0);
-  for (; s0 + 2 <= shares; s0 += 2) add(std::integral_constant<int, 2>{}, s0);
-  if (s0 < shares) add(std::integral_constant<int, 1>{}, s0);
+  }
   const float inv = sum > 0.f ? 1.f / sum : 0.f;
   if (on) {
     const uint16_t x = __builtin_bit_cast(uint16_t, (__bf16)(a0 * inv));
