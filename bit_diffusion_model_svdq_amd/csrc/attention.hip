@@ -746,7 +746,7 @@ __global__ __launch_bounds__(256) void attention_join(const Params p, int rows_p
 }
 
 // attention_keys' waves: so many that two workgroups fit a CU's LDS (a wave
-// holds two K and two V tiles).  Measured at 16 single tokens against 58.6 k
+// holds two K and two V tiles).  Measured at 16 single tokens against 49.5 k
 // keys x 8 x 128: 59.5 us with 2 waves, 61.9 with 4; 64 against 64 k keys x 16 x 64:
 // 62.9 and 53.6.
 constexpr int key_waves(int dp) { return dp == 64 ? 4 : 2; }

@@ -273,3 +273,39 @@ def test_offsets_past_the_rows_stay_inside():
     S.svdq_attention_forward(Q, K, V, cu_dev([0, 1000]), cu_dev([0, 2**31 - 1]), 0.1, False, O, None, workspace(Q, K, 1))
     torch.cuda.synchronize()
     assert torch.equal(O, want)
+
+
+def test_a_thousand_sequences():
+    """Empty, single and short sequences in no order, more than one look-up of 64 at a time."""
+    g = np.random.default_rng(7)
+    lk = g.choice([0, 1, 5, 40], 1000)
+    lq = np.minimum(lk, g.choice([0, 1, 2], 1000))
+    run(lq, lk, 4, 2, 64, True)
+    run(lk, lk, 2, 2, 80, False)
+
+
+def test_two_calls_at_once():
+    """Two streams, each call with a workspace of its own."""
+    lens = [[700, 9, 1500], [1, 1, 1]]
+    keys = [[700, 9, 1500], [3000, 70, 4500]]
+    calls = []
+    for i in range(2):
+        cu_q, cu_k = offsets(lens[i]), offsets(keys[i])
+        Q, K, V = draw((cu_q[-1], 8, 128), 3 * i), draw((cu_k[-1], 2, 128), 3 * i + 1), draw((cu_k[-1], 2, 128), 3 * i + 2)
+        calls.append((Q, K, V, cu_dev(cu_q), cu_dev(cu_k), 0.09, True, torch.empty_like(Q), None, workspace(Q, K, 3)))
+    want = []
+    for c in calls:
+        S.svdq_attention_forward(*c)
+        torch.cuda.synchronize()
+        want.append(c[7].clone())
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        for c in calls:
+            c[7].fill_(float("nan"))
+        torch.cuda.synchronize()
+        for _ in range(5):
+            for c, s in zip(calls, streams):
+                S.svdq_attention_forward(*c, stream=s)
+        torch.cuda.synchronize()
+        for c, w in zip(calls, want):
+            assert torch.equal(c[7], w)

@@ -209,3 +209,8 @@ def test_captured_and_replayed_on_another_stream():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(x_out, want[0]) and torch.equal(h, want[1])
+
+
+def test_a_thousand_sequences():
+    lens = np.random.default_rng(7).choice([0, 0, 1, 2, 9], 1000)
+    case(list(lens), 512, "rms", "layer", True, affine=True, first=2, behind=3)

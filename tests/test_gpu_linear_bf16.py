@@ -152,3 +152,24 @@ def test_captured_and_replayed(M, K, N):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(Y, want)
+
+
+def test_two_calls_at_once():
+    """Two streams, each call with a workspace of its own (channels in shares)."""
+    calls = []
+    for i, (M, K, N) in enumerate([(130, 2048, 100), (70, 5000, 60)]):
+        Y = torch.empty(M, N, dtype=torch.bfloat16, device=DEV)
+        calls.append((draw((M, K), 2 * i), draw((N, K), 2 * i + 1, K**-0.5), None, ACTS["silu"], None, Y, workspace(M, K, N)))
+        assert calls[-1][6].numel() > 16
+    want = []
+    for c in calls:
+        S.svdq_linear_bf16_forward(*c)
+        torch.cuda.synchronize()
+        want.append(c[5].clone())
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        for c, s in zip(calls, streams):
+            S.svdq_linear_bf16_forward(*c, stream=s)
+    torch.cuda.synchronize()
+    for c, w in zip(calls, want):
+        assert torch.equal(c[5], w)
