@@ -36,6 +36,7 @@
 // rounding of p to bf16 is relative.  p is rounded to bf16 because V is bf16
 // and the MFMA takes both operands in one type; l sums the unrounded values.
 #include <algorithm>
+#include <cmath>
 
 #include "svdq_internal.h"
 
@@ -759,42 +760,94 @@ struct Plan {
   size_t part = 0, bytes = 0;
 };
 
-// attention_keys where the sequences have at most 64 rows (queries x heads of a
-// group) on average.  Else attention_rows with 4 waves, two workgroups to a CU;
-// or with 8 (256 rows), which moves half the bytes from L2, where that pays:
-// heads of more than 64 channels (the tile of a 64-channel head is one copy for
-// each of 4 waves), no causal mask (whose short tiles the finer grain balances)
-// and workgroups that fill at least 4/5 of their rounds of the CUs.  Measured
-// (8 / 4 waves): 16384 tokens x 24 x 128 2.98 / 3.05 ms; 4608 tokens (0.84 of two
-// rounds) 265 / 279 us; 4096 x 24 x 96 (0.75) 201 / 172 us; 1024 x 16 x 128
-// 45 / 32 us; packed causal prompts 200 / 197 us.
+// What a tile of 32 keys costs a workgroup, in us, by the head's size (up to 64,
+// 96, 128 channels): alone on its CU, where latency counts, and as its part of a
+// full CU; with 8 waves a workgroup has the CU to itself.  For attention_keys it
+// is a turn of all its waves.
+struct Cost {
+  double rows4, rows4_each, rows8, keys, keys_each;
+  int keys_waves;
+};
+Cost cost_of(int head_dim) {
+  if (head_dim <= 64) return {0.38, 0.30, 0, 0.46, 0.45, key_waves(64)};
+  if (head_dim <= 96) return {0.45, 0.44, 0.76, 0.75, 0.40, key_waves(128)};
+  return {0.53, 0.49, 0.90, 0.80, 0.50, key_waves(128)};
+}
+
+// The kernel, its waves and the shares of the keys by an estimate of the time for
+// sequences of the average lengths (the lengths themselves are on the device):
+// the longest chain of tiles, or all tiles over the CUs; shares add the
+// join's launch and the traffic of their partial rows, 4.3 us per million
+// channels.  The constants are measured ones.  Where the estimates differ, measured
+// (attention_rows with 4 waves / 8 waves / attention_keys): 16384 tokens x 24 x 128
+// 3.05 / 2.97 ms / -; 4608 tokens 279 / 264 us / -; 1024 x 24 x 128 24 / 34 / 38 us;
+// 1024 x 16 x 128 23 / 33 / 21; 1536 x 10 x 64 24 / - / 16; 512 causal x 32 / 8 x 128
+// 14.8 / 19.8 / 13.7.  Shares: 1024 x 24 x 128 24 us with one, 45 with two; 400
+// queries x 2 x 64 against 8000 keys 35 us with one, 14 with eight (attention_keys).
 Plan plan_of(int total_q, int total_k, int batch, int heads_q, int heads_kv, int head_dim, bool causal) {
   Plan pl;
   const int group = heads_q / heads_kv;
   const int64_t rows = (int64_t)total_q * group;
   const int64_t cus = device_cu_count();
+  const Cost cost = cost_of(head_dim);
+  const double mean_rows = (double)rows / batch, mean_q = (double)total_q / batch, mean_k = (double)total_k / batch;
+  auto estimate = [&](bool keys, int waves, int splits, double longest = 1) {
+    const double units = std::ceil(mean_rows / (keys ? kWaveRows : waves * kWaveRows)) * batch * heads_kv;
+    double each_cu = std::ceil(units * splits / cus);
+    if (keys && each_cu > 1) each_cu = 2 * std::ceil(each_cu / 2);       // two fit a CU
+    auto turns = [&](double nk) {
+      return std::ceil(std::ceil(std::ceil(nk / 32) / (keys ? cost.keys_waves : 1)) / splits);
+    };
+    // causal: half of the tiles, and their unequal lengths leave CUs waiting
+    const double seen = causal ? 1 - 0.4 * std::min(1.0, mean_q / std::max(mean_k, 1.0)) : 1;
+    const double alone = keys ? cost.keys : waves == 8 ? cost.rows8 : cost.rows4;
+    const double each = keys ? cost.keys_each : waves == 8 ? cost.rows8 : cost.rows4_each;
+    const double us = std::max(turns(longest * mean_k) * alone, turns(mean_k) * seen * each_cu * each);
+    return splits == 1 ? us : us + 4.0 + 4.3e-6 * rows * heads_kv * splits * head_dim;
+  };
   // every sequence has at most one partly filled tile
   auto tiles = [&](int height) { return std::min<int64_t>(rows / height + batch, rows); };
-  pl.keys = rows <= (int64_t)batch * 64;
-  if (!pl.keys && head_dim > 64 && !causal) {
-    const int64_t units = tiles(8 * kWaveRows) * heads_kv;
-    const int64_t slots = (units + cus - 1) / cus * cus;
-    if (5 * units >= 4 * slots) pl.waves = 8;
+  double least = 0;
+  auto offer = [&](bool keys, int waves, int splits, int chunk) {
+    const int height = keys ? kWaveRows : waves * kWaveRows;
+    // a launch with shares holds at most 4 workgroups per CU (2 of attention_rows)
+    if (splits > 1 && tiles(height) * heads_kv * splits > (keys ? 4 : 2) * cus) return;
+    const double us = estimate(keys, waves, splits);
+    if (pl.rows && us >= least) return;
+    least = us;
+    pl.keys = keys;
+    pl.waves = waves;
+    pl.rows = height;
+    pl.splits = splits;
+    pl.chunk = chunk;
+  };
+  if (rows <= (int64_t)batch * 64) {
+    // New tokens, whose sequences' lengths differ most: attention_keys, whole or in
+    // shares by each sequence's own length, so long that the two workgroups of a
+    // CU get one share each on average, 256 keys at least.  The longest is taken to be
+    // twice the average.
+    const int chunk = (int)std::max<int64_t>(256, ((int64_t)total_k * heads_kv / (2 * cus) + 127) / 128 * 128);
+    const int64_t want = 4 * cus / std::max<int64_t>(tiles(kWaveRows) * heads_kv, 1);
+    const int64_t most = std::min<int64_t>({want, ((int64_t)total_k + chunk - 1) / chunk, 64});
+    const double longest = batch > 1 ? 2 : 1;
+    offer(true, 4, 1, chunk);
+    const int mean = (int)std::min<int64_t>(most, (int64_t)std::ceil(mean_k / chunk));
+    if (most > 1 && estimate(true, 4, std::max(mean, 2), longest) < estimate(true, 4, 1, longest)) pl.splits = (int)most;
+  } else {
+    offer(false, 4, 1, 0);
+    if (head_dim > 64 && !causal) offer(false, 8, 1, 0);    // causal: the finer grain balances the tiles' lengths
+    offer(true, 4, 1, 0);
+    for (const int s : {2, 3, 4, 6, 8, 12, 16}) {
+      const int chunk = (int)std::ceil(mean_k / s);
+      if (chunk < 128) break;
+      offer(false, 4, s, chunk);
+      offer(true, 4, s, chunk);
+    }
   }
-  pl.rows = pl.keys ? kWaveRows : pl.waves * kWaveRows;
+  pl.chunk = std::max(pl.chunk, 128);
   pl.tiles = tiles(pl.rows);
-  // Shares of the keys where the tiles leave CUs idle: of 128 keys at least for
-  // attention_rows; for attention_keys as many as give the two workgroups of a
-  // CU one share each on average, 256 keys at least, and short sequences in one.
-  // A launch holds at most 4 workgroups per CU for them (2 of attention_rows).
-  const int64_t units = pl.tiles * heads_kv;
-  const int64_t want = (pl.keys ? 4 : 8 / pl.waves) * cus / std::max<int64_t>(units, 1);
-  pl.chunk = 128;
-  if (pl.keys) pl.chunk = (int)std::max<int64_t>(256, ((int64_t)total_k * heads_kv / (2 * cus) + 127) / 128 * 128);
-  const int64_t most = ((int64_t)total_k + pl.chunk - 1) / pl.chunk;
-  pl.splits = (int)std::max<int64_t>(1, std::min<int64_t>({want, most, 64}));
   if (pl.splits > 1) {
-    const size_t slots = (size_t)units * pl.splits * pl.rows;
+    const size_t slots = (size_t)pl.tiles * heads_kv * pl.splits * pl.rows;
     pl.part = (slots * head_dim * 4 + 255) & ~size_t(255);
     pl.bytes = pl.part + ((slots * 4 + 255) & ~size_t(255));
   }

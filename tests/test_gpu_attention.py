@@ -95,6 +95,15 @@ def test_head_groups(hq, hkv):
     run([70, 3, 129], [70, 3, 129], hq, hkv, 64, True)
 
 
+@pytest.mark.parametrize("d", [8, 40, 64, 72, 96, 128])
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("lens,hkv", [([127, 0, 130, 5, 129], 96), ([300, 1, 130], 96), ([257, 255], 96),
+                                      ([65, 200, 31], 24), ([500, 333, 0, 129], 48)])
+def test_many_heads(lens, hkv, causal, d):
+    """Enough tiles that attention_rows takes them, with 4 and with 8 waves."""
+    run(lens, lens, 96, hkv, d, causal)
+
+
 @pytest.mark.parametrize("causal", [False, True])
 @pytest.mark.parametrize("lq,lk", [
     ([40, 200], [7, 1]),            # causal: the first queries see no key
@@ -123,6 +132,9 @@ def test_a_long_sequence_is_cut_into_shares():
     assert S.svdq_attention_workspace_bytes(200, 4000, 1, 2, 2, 64) > 0
     run([200], [4000], 2, 2, 64, False)
     run([200], [4000], 2, 2, 128, True)
+    for d in (64, 96, 128):
+        run([100, 0, 80], [5000, 9, 1003], 24, 24, d, d == 96)
+        run([100], [5000], 24, 24, d, d == 128)
     assert S.svdq_attention_workspace_bytes(1, 5000, 1, 8, 2, 128) > 0
     run([1], [5000], 8, 2, 128, True)
 
