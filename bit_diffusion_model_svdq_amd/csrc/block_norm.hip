@@ -14,7 +14,8 @@
 // HBM bound: 2 (or 4) + 2 bytes in and as many out per element, a few
 // operations each.  A row belongs to W waves, W the smallest power of two
 // that leaves a thread at most kMaxVec chunks of 8 channels; with W = 1 a
-// workgroup holds four rows and runs without barriers.
+// workgroup of four waves runs without barriers, and rows of up to 256 channels
+// share a wave (L lanes each): 100000 x 128 19.4 us, 46 with a wave per row.
 #include "svdq_internal.h"
 
 namespace svdq {
@@ -63,11 +64,11 @@ __device__ inline void store8(float* p, const float (&f)[8]) {
   __builtin_nontemporal_store(f32x4{f[4], f[5], f[6], f[7]}, reinterpret_cast<f32x4*>(p + 4));
 }
 
-// The sum of v over the row's W waves, in every thread (the same order in each).
-template <int W>
+// The sum of v over the row's L lanes or W waves, in every thread (the same order in each).
+template <int W, int L>
 __device__ inline float row_sum(float v, float* lds, int wave) {
 #pragma unroll
-  for (int s = 32; s > 0; s >>= 1) v += __shfl_xor(v, s);
+  for (int s = L / 2; s > 0; s >>= 1) v += __shfl_xor(v, s);
   if constexpr (W > 1) {
     if ((threadIdx.x & 63) == 0) lds[wave] = v;
     __syncthreads();
@@ -80,7 +81,7 @@ __device__ inline float row_sum(float v, float* lds, int wave) {
 }
 
 // Normalises the row in place (chunks past the row hold 0 and stay 0).
-template <int W, int V>
+template <int W, int L, int V>
 __device__ inline void normalise(float (&v)[V][8], const bool (&ok)[V], int kind, float eps, float inv_width,
                                  float* lds, int wave) {
   if (kind == kNormNone) return;
@@ -90,7 +91,7 @@ __device__ inline void normalise(float (&v)[V][8], const bool (&ok)[V], int kind
     for (int i = 0; i < V; ++i)
 #pragma unroll
       for (int e = 0; e < 8; ++e) s += v[i][e];
-    const float mean = row_sum<W>(s, lds, wave) * inv_width;
+    const float mean = row_sum<W, L>(s, lds, wave) * inv_width;
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
@@ -101,7 +102,7 @@ __device__ inline void normalise(float (&v)[V][8], const bool (&ok)[V], int kind
   for (int i = 0; i < V; ++i)
 #pragma unroll
     for (int e = 0; e < 8; ++e) q = __builtin_fmaf(v[i][e], v[i][e], q);
-  const float r = rsqrtf(__builtin_fmaf(row_sum<W>(q, lds, wave), inv_width, eps));
+  const float r = rsqrtf(__builtin_fmaf(row_sum<W, L>(q, lds, wave), inv_width, eps));
 #pragma unroll
   for (int i = 0; i < V; ++i)
 #pragma unroll
@@ -125,22 +126,24 @@ __device__ inline int sequence_of(const int32_t* cu, int batch, int64_t row) {
 
 // x and x_out, y and h may be the same buffers: a thread writes only the
 // chunks that it has itself read before.
-template <class S, int W, int V>
+template <class S, int W, int L, int V>
 __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void block_norm_kernel(const BlockNormArgs a) {
   __shared__ float lds[W == 1 ? 1 : W];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t row = W == 1 ? (int64_t)blockIdx.x * 4 + wave : blockIdx.x;
+  const int64_t row = W > 1 ? (int64_t)blockIdx.x
+                      : L == 64 ? (int64_t)blockIdx.x * 4 + wave
+                                : (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
   if (row >= a.rows) return;
   const int b = sequence_of(a.cu, a.batch, row);
   if (b < 0) return;
-  const int t = W == 1 ? threadIdx.x & 63 : threadIdx.x;
+  const int t = W == 1 ? threadIdx.x % L : threadIdx.x;
   const int64_t at = row * a.width;
   const float inv_width = 1.0f / (float)a.width;
   int ch[V];
   bool ok[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    ch[i] = 8 * (t + i * 64 * W);
+    ch[i] = 8 * (t + i * L * W);
     ok[i] = ch[i] < a.width;
   }
   float x[V][8], y[V][8];
@@ -152,7 +155,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void block_norm_kernel(const
     if (ok[i] && a.y) load8(a.y + at + ch[i], y[i]);
   }
   if (a.y) {
-    normalise<W, V>(y, ok, a.post, a.eps, inv_width, lds, wave);
+    normalise<W, L, V>(y, ok, a.post, a.eps, inv_width, lds, wave);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       if (!ok[i]) continue;
@@ -178,7 +181,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void block_norm_kernel(const
     for (int i = 0; i < V; ++i)
       if (ok[i]) store8(static_cast<S*>(a.x_out) + at + ch[i], x[i]);
   if (!a.h) return;
-  normalise<W, V>(x, ok, a.pre, a.eps, inv_width, lds, wave);
+  normalise<W, L, V>(x, ok, a.pre, a.eps, inv_width, lds, wave);
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     if (!ok[i]) continue;
@@ -207,25 +210,28 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void block_norm_kernel(const
   }
 }
 
-template <class S, int W, int V>
+template <class S, int W, int L, int V>
 hipError_t launch(const BlockNormArgs& a, hipStream_t stream) {
-  const int64_t blocks = W == 1 ? (a.rows + 3) / 4 : a.rows;
-  hipLaunchKernelGGL((block_norm_kernel<S, W, V>), dim3((unsigned)blocks), dim3(W == 1 ? 256 : 64 * W), 0, stream, a);
+  constexpr int kRows = W == 1 ? 256 / L : 1;      // of a workgroup
+  const int64_t blocks = (a.rows + kRows - 1) / kRows;
+  hipLaunchKernelGGL((block_norm_kernel<S, W, L, V>), dim3((unsigned)blocks), dim3(W == 1 ? 256 : 64 * W), 0, stream, a);
   return hipGetLastError();
 }
 
 template <class S, int W>
 hipError_t with_vec(const BlockNormArgs& a, hipStream_t stream) {
   const int v = (a.width / 8 + 64 * W - 1) / (64 * W);
-  if (v <= 1) return launch<S, W, 1>(a, stream);
-  if (v == 2) return launch<S, W, 2>(a, stream);
-  if (v == 3) return launch<S, W, 3>(a, stream);
-  return launch<S, W, 4>(a, stream);
+  if (v <= 1) return launch<S, W, 64, 1>(a, stream);
+  if (v == 2) return launch<S, W, 64, 2>(a, stream);
+  if (v == 3) return launch<S, W, 64, 3>(a, stream);
+  return launch<S, W, 64, 4>(a, stream);
 }
 
 template <class S>
 hipError_t with_waves(const BlockNormArgs& a, hipStream_t stream) {
   const int chunks = a.width / 8;
+  if (chunks <= 16) return launch<S, 1, 16, 1>(a, stream);
+  if (chunks <= 32) return launch<S, 1, 32, 1>(a, stream);
   if (chunks <= 64 * kMaxVec) return with_vec<S, 1>(a, stream);
   if (chunks <= 128 * kMaxVec) return with_vec<S, 2>(a, stream);
   if (chunks <= 256 * kMaxVec) return with_vec<S, 4>(a, stream);

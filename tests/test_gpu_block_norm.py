@@ -214,3 +214,11 @@ def test_captured_and_replayed_on_another_stream():
 def test_a_thousand_sequences():
     lens = np.random.default_rng(7).choice([0, 0, 1, 2, 9], 1000)
     case(list(lens), 512, "rms", "layer", True, affine=True, first=2, behind=3)
+
+
+@pytest.mark.parametrize("width", [8, 64, 120, 128, 136, 200, 256, 264])
+@pytest.mark.parametrize("post,pre", [("none", "layer"), ("rms", "rms"), ("layer", "none")])
+def test_narrow_rows_share_a_wave(width, post, pre):
+    """Rows of up to 256 channels: several to a wave, of different sequences, some outside them."""
+    case([3, 0, 1, 30, 2, 5], width, post, pre, affine=True, first=3, behind=5)
+    case([1, 1, 1, 1, 1], width, post, pre, fp32=True, first=1, behind=70)
