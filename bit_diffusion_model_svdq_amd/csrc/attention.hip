@@ -15,7 +15,8 @@
 //                   K/V tile.
 //   attention_keys  a workgroup takes 32 rows in all; its waves take alternate
 //                   K/V tiles and join at the end.  For few rows per
-//                   sequence, where the keys' bytes are what counts.
+//                   sequence, where the keys' bytes are what counts, and for
+//                   launches whose larger tiles would leave CUs idle.
 // Where the tiles do not fill the chip, each tile's keys are cut into
 // `splits` shares; shares write float32 partial rows and attention_join
 // brings them together.
