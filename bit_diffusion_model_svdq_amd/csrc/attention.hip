@@ -5,7 +5,8 @@
 // over the keys j of query i's own sequence (causal: j <= i + nk - nq, so the
 // last query sees the last key), in one pass over the keys with the running
 // maximum m and sum l of the softmax.  A query without keys gets O = 0 and
-// log-sum-exp -inf.
+// log-sum-exp -inf; one with a NaN or +inf among its scores, or with none in
+// float32's range, gets NaN in both.
 //
 // Work split.  The `group` query heads that share a key head are rows of one
 // problem: row r of (sequence, key head) is token r / group, head r % group.
@@ -72,7 +73,7 @@ struct Params {
   int tiles;             // of the launch (at least those of the batch)
   int splits, chunk;     // a sequence's keys are cut into shares of about `chunk` keys, at most `splits`
   float* part;           // [unit][rows][head_dim] partial rows, unit = (share, tile, key head)
-  float* part_lse;       // [unit][rows], base 2; -inf: the share saw no key
+  float* part_lse;       // [unit][rows], base 2; -inf: the share has no weight, and no row
 
   __device__ int shares(int nk) const { return min(max((nk + chunk - 1) / chunk, 1), splits); }
 };
@@ -343,11 +344,12 @@ struct Work {
   __device__ bool whole(int t) const { return t * T::KT + T::KT <= wfull; }
 
   // Moves to the maximum `top` of a tile to come where, somewhere in the wave,
-  // it exceeds the one in use by more than kLazy.
+  // it exceeds the one in use by more than kLazy.  A maximum below float32's range
+  // (and a NaN) is none: m c stays above -inf.
   __device__ void follow(float top) {
     top = max_halves(top);
     if (__any(top * p.c > __builtin_fmaf(m, p.c, kLazy))) {
-      const float mn = fmaxf(m, top);
+      const float mn = fmaxf(m, top * p.c > -INFINITY ? top : -INFINITY);
       const float f = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m - mn) * p.c);
       m = mn;
       l *= f;
@@ -359,15 +361,28 @@ struct Work {
   }
 
   // The rows' results: to O and lse, or to this share's slots of the workspace.
+  // A sum of 0 stands for no weight at all, and only that: a NaN or infinite
+  // score makes the sum NaN, which goes on into O and lse.  No weight is
+  // right for a query that sees no key.  Where it does see some, their scores
+  // all left float32's range (scale log2(e) times the maximum is infinite, or
+  // every score is -inf), and the result is NaN; a share whose scores are all
+  // -inf is like an empty one, and the join decides.
   __device__ void finish() {
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    const float lse2 = l > 0.f ? __builtin_fmaf(m, p.c, __builtin_amdgcn_logf(l)) : -INFINITY;
+    const bool none = l == 0.f;
+    const bool lost = none && (shares > 1 ? m * p.c == INFINITY : seen > 0);
+    const float inv = lost ? NAN : none ? 0.f : 1.f / l;
+    const float lse2 = lost ? NAN : none ? -INFINITY : __builtin_fmaf(m, p.c, __builtin_amdgcn_logf(l));
     if (!row_ok) return;
+    if (none)                      // V's infinities and NaN times no weight
+#pragma unroll
+      for (int i = 0; i < H::DB; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) o[i][j] = 0.f;
     if (shares > 1) {
       const int64_t slot = (int64_t)blockIdx.x * T::ROWS + (row - row0);
       if (half == 0) p.part_lse[slot] = lse2;
       float* dst = p.part + slot * p.head_dim;
-      if (l > 0.f) {
+      if (!none) {
 #pragma unroll
         for (int i = 0; i < H::DB; ++i)
 #pragma unroll
@@ -685,7 +700,8 @@ __global__ __launch_bounds__(NW * 64, 2) void attention_keys(const Params p) {
 
 // Joins the shares of a tile's rows: weights 2^(lse_s - max), rows summed in
 // share order in float32.  One wave per row: lane s holds share s's weight (at
-// most 64 shares), then each lane two channels, eight shares at a time.
+// most 64 shares), then each lane two channels, eight shares at a time.  A NaN
+// lse_s passes the maximum by and makes its weight, the sum and the row NaN.
 __global__ __launch_bounds__(256) void attention_join(const Params p, int rows_per_tile) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -729,13 +745,16 @@ __global__ __launch_bounds__(256) void attention_join(const Params p, int rows_p
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       const float w = __shfl(weight, (s0 + u) & 63);
-      if (s0 + u < shares && w > 0.f) {                  // a share without weight has written nothing
+      if (s0 + u < shares && w != 0.f) {                 // a share without weight has written nothing
         a0 = __builtin_fmaf(w, v[u].x, a0);
         a1 = __builtin_fmaf(w, v[u].y, a1);
       }
     }
   }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  // as in finish(): no weight at all is NaN for a query that sees keys
+  const int seen = p.causal ? min(token + at.nk - at.nq + 1, at.nk) : at.nk;
+  const bool none = sum == 0.f;
+  const float inv = !none ? 1.f / sum : seen > 0 ? NAN : 0.f;
   if (on) {
     const uint16_t x = __builtin_bit_cast(uint16_t, (__bf16)(a0 * inv));
     const uint16_t y = __builtin_bit_cast(uint16_t, (__bf16)(a1 * inv));
@@ -744,7 +763,7 @@ __global__ __launch_bounds__(256) void attention_join(const Params p, int rows_p
   }
   if (p.lse && lane == 0)
     p.lse[(int64_t)head * p.total_q + at.q0 + token] =
-        sum > 0.f ? (top + __builtin_amdgcn_logf(sum)) * kLn2 : -INFINITY;
+        !none ? (top + __builtin_amdgcn_logf(sum)) * kLn2 : seen > 0 ? NAN : -INFINITY;
 }
 
 // attention_keys' waves: so many that two workgroups fit a CU's LDS (a wave

@@ -401,11 +401,17 @@ size_t svdq_attention_workspace_bytes(int64_t total_q, int64_t total_k, int batc
  * j <= i + nk - nq of nk, so that the last query sees the last key.
  * A query that sees no key gets O = 0 and log-sum-exp -inf.
  * lse (float32 [heads_q, total_q], may be NULL): ln sum_j exp(scale Q . K).
+ * Scores are float32 numbers: Q . K first, then times scale log2(e).  A query with
+ * a NaN among the scores it sees, or one that is +inf or overflows above, gets NaN
+ * in O and lse; a score that is -inf or overflows below weighs nothing, and a query
+ * all of whose scores do gets NaN too.  Non-finite elements of a row of Q thus
+ * reach that row and head alone.
  * Requires head_dim a multiple of 8 up to 128 and ldk, ldv up to 2^24 (above:
  * SVDQ_ERR_UNSUPPORTED),
- * heads_q a multiple of heads_kv, scale positive and at most 2^126.  Non-finite K or
- * V elements can reach every query of their sequence and key head, also the
- * queries that the causal mask hides them from, but no other sequence.
+ * heads_q a multiple of heads_kv, scale positive and at most 2^126.  Non-finite
+ * elements of K and V reach every query that sees their key (O there is not finite;
+ * lse by K alone); they can also reach queries of their sequence and key head that
+ * the causal mask hides them from and that see other keys, but no other sequence.
  * The sums run in an order that depends on the shapes only, so equal calls
  * give equal bits. */
 svdq_status svdq_attention_forward(const uint16_t* Q, int64_t ldq, const uint16_t* K, int64_t ldk,
