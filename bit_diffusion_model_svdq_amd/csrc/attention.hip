@@ -37,6 +37,14 @@
 // which leaves p <= 2^8: exact sums in float32, and the
 // rounding of p to bf16 is relative.  p is rounded to bf16 because V is bf16
 // and the MFMA takes both operands in one type; l sums the unrounded values.
+// With few rows per sequence (new tokens) p goes in two bf16 parts instead, the
+// upper 16 bits and the rounded rest: O is then as good as its own rounding
+// (Frobenius error against float64 1.66e-3; 2.0e-3 to 2.3e-3 with one part).  There
+// the keys' bytes are what counts: 16 single tokens 46.2 -> 48.3 us, 64 against
+// 64 k keys 47.8 -> 48.2, one against 32 k 34.1 -> 34.4 (graph).  Elsewhere the second MFMA
+// of P V costs more than those digits are worth: 16384 tokens x 24 x 128 2.93 -> 4.13 ms,
+// 4608 tokens 268 -> 362 us, and in attention_keys 1024 x 16 x 128 23.2 -> 26.2 us,
+// 1536 x 10 x 64 15.7 -> 18.3.
 #include <algorithm>
 #include <cmath>
 
@@ -579,8 +587,9 @@ __global__ __launch_bounds__(NW * 64, 2) void attention_rows(const Params p) {
 }
 
 // Few rows: all waves have the same 32 rows and take every NW-th tile, each in
-// buffers of its own, without barriers until they join.
-template <class H, int NW>
+// buffers of its own, without barriers until they join.  PARTS: of a weight in
+// the product with V.
+template <class H, int NW, int PARTS>
 __global__ __launch_bounds__(NW * 64, 2) void attention_keys(const Params p) {
   using T = Tile<H, kKeys, NW>;
   __shared__ __attribute__((aligned(16))) uint8_t k0s[T::BUFS * T::TILE_BYTES];
@@ -603,18 +612,32 @@ __global__ __launch_bounds__(NW * 64, 2) void attention_keys(const Params p) {
     if (!w.whole(t)) w.mask(s, t);
     w.follow(highest(s));
     const float mc = w.m == -INFINITY ? 0.f : -w.m * p.c;
-    bf16x8 pf[2];
+    bf16x8 pf[2], rest[2];
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
       const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j], p.c, mc));
       w.l += e;
-      pf[j >> 3][j & 7] = (__bf16)e;
+      if constexpr (PARTS == 2) {
+        const uint32_t upper = __float_as_uint(e) >> 16;
+        pf[j >> 3][j & 7] = __builtin_bit_cast(__bf16, (uint16_t)upper);
+        rest[j >> 3][j & 7] = (__bf16)(e - __uint_as_float(upper << 16));
+      } else {
+        pf[j >> 3][j & 7] = (__bf16)e;
+      }
     }
 #pragma unroll
-    for (int st = 0; st < 2; ++st)
+    for (int st = 0; st < 2; ++st) {
+      bf16x8 vf[H::DB];
 #pragma unroll
-      for (int db = 0; db < H::DB; ++db)
-        w.o[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w.v_frag(vt, st, db), pf[st], w.o[db], 0, 0, 0);
+      for (int db = 0; db < H::DB; ++db) {
+        vf[db] = w.v_frag(vt, st, db);
+        w.o[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[db], pf[st], w.o[db], 0, 0, 0);
+      }
+      if constexpr (PARTS == 2)
+#pragma unroll
+        for (int db = 0; db < H::DB; ++db)
+          w.o[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[db], rest[st], w.o[db], 0, 0, 0);
+    }
   };
   int t = w.t0 + wave;
   w.start(t);
@@ -772,8 +795,12 @@ __global__ __launch_bounds__(256) void attention_join(const Params p, int rows_p
 // 62.9 and 53.6.
 constexpr int key_waves(int dp) { return dp == 64 ? 4 : 2; }
 
+// Rows per sequence, on average, up to which a call counts as one of new tokens.
+constexpr int kTokenRows = 64;
+
 struct Plan {
   bool keys = false;      // attention_keys: 32 rows per workgroup
+  int parts = 1;          // of a weight in P V
   int waves = 4;          // of a workgroup
   int rows = 0, splits = 1, chunk = 0;
   int64_t tiles = 0;      // at most, over the packed batch
@@ -841,7 +868,8 @@ Plan plan_of(int total_q, int total_k, int batch, int heads_q, int heads_kv, int
     pl.splits = splits;
     pl.chunk = chunk;
   };
-  if (rows <= (int64_t)batch * 64) {
+  if (rows <= (int64_t)batch * kTokenRows) {
+    pl.parts = 2;
     // New tokens, whose sequences' lengths differ most: attention_keys, whole or in
     // shares by each sequence's own length, so long that the two workgroups of a
     // CU get one share each on average, 256 keys at least.  The longest is taken to be
@@ -879,7 +907,10 @@ hipError_t launch(const Plan& pl, const Params& p, hipStream_t stream) {
   const dim3 grid((unsigned)(pl.tiles * p.heads_kv * pl.splits));
   if (pl.keys) {
     constexpr int kWaves = key_waves(H::DP);
-    hipLaunchKernelGGL((attention_keys<H, kWaves>), grid, dim3(kWaves * 64), 0, stream, p);
+    if (pl.parts == 2)
+      hipLaunchKernelGGL((attention_keys<H, kWaves, 2>), grid, dim3(kWaves * 64), 0, stream, p);
+    else
+      hipLaunchKernelGGL((attention_keys<H, kWaves, 1>), grid, dim3(kWaves * 64), 0, stream, p);
   } else if (pl.waves == 8) {
     if constexpr (H::DP == 128)
       hipLaunchKernelGGL((attention_rows<H, 8>), grid, dim3(512), 0, stream, p);

@@ -390,7 +390,8 @@ size_t svdq_attention_workspace_bytes(int64_t total_q, int64_t total_k, int batc
 /* Softmax attention of every query over the keys of its own sequence:
  *   O[i, h] = sum_j softmax_j(scale Q[i, h] . K[j, h / G]) V[j, h / G],  G = heads_q / heads_kv
  * bf16 in and out, products, softmax and sums in float32; the softmax's
- * weights enter the product with V rounded to bf16 (the values' type).
+ * weights enter the product with V rounded to bf16 (the values' type), and with
+ * 15 bits where the call has at most 64 rows (total_q times G) per sequence.
  *   Q [total_q, heads_q, head_dim], K, V [total_k, heads_kv, head_dim],
  *   O [total_q, heads_q, head_dim]: rows ldq, ldk, ldv, ldo elements apart
  *   (multiples of 8, so column slices of one projection's output serve as
