@@ -83,7 +83,7 @@ struct Params {
   float* part;           // [unit][rows][head_dim] partial rows, unit = (share, tile, key head)
   float* part_lse;       // [unit][rows], base 2; -inf: the share has no weight, and no row
 
-  __device__ int shares(int nk) const { return min(max((nk + chunk - 1) / chunk, 1), splits); }
+  __device__ int shares(int nk) const { return min(nk > 0 ? (nk - 1) / chunk + 1 : 1, splits); }
 };
 
 // One head's geometry: DP the LDS row in channels, KS the MFMA steps of 16

@@ -280,8 +280,10 @@ svdq_status check_attention_shape(int batch, int64_t total_q, int64_t total_k, i
   if (head_dim < 8 || head_dim % 8)
     return fail(SVDQ_ERR_INVALID_ARG, "head_dim must be a positive multiple of 8 (got %d)", head_dim);
   if (head_dim > 128) return fail(SVDQ_ERR_UNSUPPORTED, "head_dim %d is above 128", head_dim);
-  if (total_q > INT32_MAX || total_k > INT32_MAX || total_q * (heads_q / heads_kv) > INT32_MAX - 512)
-    return fail(SVDQ_ERR_INVALID_ARG, "total_q=%lld (times %d heads a group) or total_k=%lld is beyond 31 bits",
+  // the kernels count rows and keys in 32 bits: up to the end of a tile that the last one
+  // begins (rows), and of the four tiles that are copied or looked at ahead (keys)
+  if (total_q > INT32_MAX || total_k > INT32_MAX - 512 || total_q * (heads_q / heads_kv) > INT32_MAX - 512)
+    return fail(SVDQ_ERR_INVALID_ARG, "total_q=%lld (times %d heads a group) or total_k=%lld is beyond 31 bits less 512",
                 (long long)total_q, heads_q / heads_kv, (long long)total_k);
   if (total_q > 0 && attention_blocks((int)total_q, (int)total_k, batch, heads_q, heads_kv, head_dim) > kMaxBlocks)
     return fail(SVDQ_ERR_INVALID_ARG, "too many rows for one launch: total_q=%lld, heads_q=%d, batch=%d",
