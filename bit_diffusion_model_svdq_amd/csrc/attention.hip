@@ -874,7 +874,8 @@ Plan plan_of(int total_q, int total_k, int batch, int heads_q, int heads_kv, int
     // shares by each sequence's own length, so long that the two workgroups of a
     // CU get one share each on average, 256 keys at least.  The longest is taken to be
     // twice the average.
-    const int chunk = (int)std::max<int64_t>(256, ((int64_t)total_k * heads_kv / (2 * cus) + 127) / 128 * 128);
+    const int64_t fair = ((int64_t)total_k * heads_kv / (2 * cus) + 127) / 128 * 128;
+    const int chunk = (int)std::max<int64_t>(256, std::min<int64_t>(fair, total_k));     // with many key heads: one share
     const int64_t want = 4 * cus / std::max<int64_t>(tiles(kWaveRows) * heads_kv, 1);
     const int64_t most = std::min<int64_t>({want, ((int64_t)total_k + chunk - 1) / chunk, 64});
     const double longest = batch > 1 ? 2 : 1;

@@ -29,3 +29,11 @@ def test_the_most_keys_are_taken():
     """As far as the workspace, which is too small here."""
     assert S.svdq_attention_workspace_bytes(1, MOST, 1, 1, 1, 8) > 16
     assert attention(total_k=MOST) == WORKSPACE
+
+
+@pytest.mark.parametrize("total_k,heads", [(2**22, 2**19), (2**20, 2**20), (MOST, 2**9), (2**28, 2**13 - 1), (300, 2**20)])
+def test_many_keys_of_many_heads_make_one_share(total_k, heads):
+    """Keys x heads beyond 32 bits: the plan is made in 64."""
+    assert S.svdq_attention_workspace_bytes(1, total_k, 1, heads, heads, 8) == 0
+    wide = heads * 8
+    assert attention(total_k=total_k, heads_q=heads, heads_kv=heads, ldq=wide, ldk=wide, ldv=wide, ldo=wide, Q=None) == INVALID
