@@ -684,10 +684,13 @@ def _need_heads(t, name, index=None, head_dim=None, rows=None, heads=None):
     return ld if n > 1 else h * d
 
 
-def _need_tensors(**ts):
-    """TypeError for the first operand that is neither a tensor nor None."""
+def _need_tensors(required, **ts):
+    """Names the first operand that is None though `required` (names), or no tensor."""
     for name, t in ts.items():
-        if not (t is None or hasattr(t, "data_ptr") and hasattr(t, "get_device")):
+        if t is None:
+            if name in required:
+                raise ValueError(f"{name} must not be None")
+        elif not (hasattr(t, "data_ptr") and hasattr(t, "get_device")):
             raise TypeError(f"{name} must be a torch tensor on the GPU")
 
 
@@ -734,8 +737,9 @@ def svdq_attention_forward(Q, K, V, cu_q, cu_k, scale, causal, O, lse=None, work
             _same_device(Q, K, V, O, cu_q, cu_k, lse, workspace)
         if workspace is not None and not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
-    except AttributeError:
-        _need_tensors(Q=Q, K=K, V=V, O=O, cu_q=cu_q, cu_k=cu_k, lse=lse, workspace=workspace)
+    except (AttributeError, IndexError):
+        _need_tensors(("Q", "K", "V", "O"), Q=Q, K=K, V=V, O=O, cu_q=cu_q, cu_k=cu_k, lse=lse, workspace=workspace)
+        _need_cu(cu_q, "cu_q")
         raise
     _launch(index, stream, _lib.svdq_attention_forward, Q.data_ptr(), ldq, K.data_ptr(), ldk, V.data_ptr(), ldv,
             _ptr(cu_q), _ptr(cu_k), batch, total_q, total_k, heads_q, heads_kv, d, scale, int(causal), O.data_ptr(), ldo,
@@ -789,9 +793,10 @@ def svdq_block_norm_forward(x, y, cu, post, post_weight, gate, residual_scale, b
         ld_gate = _need_vectors(gate, "gate", batch, width, index)
         ld_scale = _need_vectors(scale, "scale", batch, width, index)
         ld_shift = _need_vectors(shift, "shift", batch, width, index)
-    except AttributeError:
-        _need_tensors(x=x, y=y, cu=cu, post_weight=post_weight, gate=gate, pre_weight=pre_weight, pre_bias=pre_bias,
+    except (AttributeError, IndexError):
+        _need_tensors(("x",), x=x, y=y, cu=cu, post_weight=post_weight, gate=gate, pre_weight=pre_weight, pre_bias=pre_bias,
                       scale=scale, shift=shift, x_out=x_out, h=h)
+        _need_cu(cu, "cu")
         raise
     _launch(index, stream, _lib.svdq_block_norm_forward, x.data_ptr(), SVDQ_F32 if f32 else SVDQ_BF16, _ptr(y), rows,
             width, _ptr(cu), batch, post, _ptr(post_weight), _ptr(gate), ld_gate, residual_scale, branch_scale, pre,
@@ -825,7 +830,7 @@ def svdq_linear_bf16_forward(X, W, bias, activation, residual, Y, workspace=None
         if workspace is not None and not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
     except AttributeError:
-        _need_tensors(X=X, W=W, bias=bias, residual=residual, Y=Y, workspace=workspace)
+        _need_tensors(("X", "W", "Y"), X=X, W=W, bias=bias, residual=residual, Y=Y, workspace=workspace)
         raise
     _launch(index, stream, _lib.svdq_linear_bf16_forward, X.data_ptr(), M, K, N, W.data_ptr(), _ptr(bias),
             int(activation), _ptr(residual), Y.data_ptr(), SVDQ_F32 if f32 else SVDQ_BF16, _ptr(workspace),
