@@ -221,8 +221,10 @@ hipError_t launch(const BlockNormArgs& a, hipStream_t stream) {
 template <class S, int W>
 hipError_t with_vec(const BlockNormArgs& a, hipStream_t stream) {
   const int v = (a.width / 8 + 64 * W - 1) / (64 * W);
-  if (v <= 1) return launch<S, W, 64, 1>(a, stream);
-  if (v == 2) return launch<S, W, 64, 2>(a, stream);
+  if constexpr (W == 1) {      // with more waves a thread has three chunks at least
+    if (v <= 1) return launch<S, W, 64, 1>(a, stream);
+    if (v == 2) return launch<S, W, 64, 2>(a, stream);
+  }
   if (v == 3) return launch<S, W, 64, 3>(a, stream);
   return launch<S, W, 64, 4>(a, stream);
 }
