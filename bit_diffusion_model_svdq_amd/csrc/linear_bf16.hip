@@ -499,7 +499,9 @@ __global__ __launch_bounds__(256) void linear_join(const LinearArgs a) {
 // kRowWaves-th block of 64 channels.  Lane (fk, fr) reads 32 neighbouring
 // bytes of weight row fr, so that the four lanes of a row take a whole
 // 128-byte line; the MFMA's k slots are any 32 channels as long as both
-// operands agree, so the two 16-byte halves are two MFMAs.  (From 17 rows on the
+// operands agree, so the two 16-byte halves are two MFMAs.  The loop is not
+// unrolled: a wave has one block's loads in flight, and the waves of a CU make up
+// for it where N gives it several workgroups.  (From 17 rows on the
 // tiles are faster: 32 x 3072 -> 18432 31 us in 64 x 64 tiles with two shares,
 // 54 us here with two blocks of rows.)
 constexpr int kRowsMax = 16;
@@ -516,7 +518,6 @@ __global__ __launch_bounds__(kRowWaves * 64) void linear_rows(const LinearArgs a
   f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
   const int blocks = (a.K + 63) / 64;
   const u32x4 zero = u32x4{0u, 0u, 0u, 0u};
-#pragma unroll 4
   for (int kb = wave; kb < blocks; kb += kRowWaves) {
     const int k = 64 * kb + 16 * fk;
 #pragma unroll
