@@ -588,9 +588,10 @@ __global__ __launch_bounds__(NW * 64, 2) void attention_rows(const Params p) {
 
 // Few rows: all waves have the same 32 rows and take every NW-th tile, each in
 // buffers of its own, without barriers until they join.  PARTS: of a weight in
-// the product with V.
+// the product with V.  Heads of more than 64 channels take the registers of a whole
+// SIMD, and two workgroups of two waves the LDS of a CU.
 template <class H, int NW, int PARTS>
-__global__ __launch_bounds__(NW * 64, 2) void attention_keys(const Params p) {
+__global__ __launch_bounds__(NW * 64, H::DP == 64 ? 2 : 1) void attention_keys(const Params p) {
   using T = Tile<H, kKeys, NW>;
   __shared__ __attribute__((aligned(16))) uint8_t k0s[T::BUFS * T::TILE_BYTES];
   __shared__ __attribute__((aligned(16))) uint8_t k1s[T::BUFS * T::TILE_BYTES];
