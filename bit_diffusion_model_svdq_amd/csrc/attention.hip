@@ -40,9 +40,9 @@
 // With few rows per sequence (new tokens) p goes in two bf16 parts instead, the
 // upper 16 bits and the rounded rest: O is then as good as its own rounding
 // (Frobenius error against float64 1.66e-3; 2.0e-3 to 2.3e-3 with one part).  There
-// the keys' bytes are what counts: 16 single tokens 46.2 -> 48.3 us, 64 against
-// 64 k keys 47.8 -> 48.2, one against 32 k 34.1 -> 34.4 (graph).  Elsewhere the second MFMA
-// of P V costs more than those digits are worth: 16384 tokens x 24 x 128 2.93 -> 4.13 ms,
+// the keys' bytes are what counts: 16 single tokens 56.4 -> 56.8 us, 64 against 64 k keys
+// 59.3 -> 59.6 (46.2 -> 48.3 and 47.8 -> 48.2 with the keys in the Infinity Cache, one
+// against 32 k 34.1 -> 34.4).  Elsewhere the second MFMA of P V costs more than those digits are worth: 16384 tokens x 24 x 128 2.93 -> 4.13 ms,
 // 4608 tokens 268 -> 362 us, and in attention_keys 1024 x 16 x 128 23.2 -> 26.2 us,
 // 1536 x 10 x 64 15.7 -> 18.3.
 #include <algorithm>
@@ -791,9 +791,9 @@ __global__ __launch_bounds__(256) void attention_join(const Params p, int rows_p
 }
 
 // attention_keys' waves: so many that two workgroups fit a CU's LDS (a wave
-// holds two K and two V tiles).  Measured at 16 single tokens against 49.5 k
-// keys x 8 x 128: 59.5 us with 2 waves, 61.9 with 4; 64 against 64 k keys x 16 x 64:
-// 62.9 and 53.6.
+// holds two K and two V tiles).  Measured with keys from HBM: 16 single tokens against
+// 49.5 k keys x 8 x 128 56.8 us with 2 waves, 60.6 with 4, 32 against 64 k x 16 x 80
+// 85.2 and 91.1; 64 against 64 k x 16 x 64 59.0 and 59.5.
 constexpr int key_waves(int dp) { return dp == 64 ? 4 : 2; }
 
 // Rows per sequence, on average, up to which a call counts as one of new tokens.

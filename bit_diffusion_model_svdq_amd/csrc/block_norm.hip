@@ -55,9 +55,9 @@ __device__ inline void load8(const float* p, float (&f)[8]) {
     f[4 + i] = b[i];
   }
 }
-// Non-temporal: x' and h stream out to HBM.  4608 x 3072 bf16 20.6 us (5.5 TB/s)
-// against 29.4 with stores that allocate in the caches, 29484 x 1280 float32
-// 90.8 (5.0 TB/s) against 97.9; loads of x and y gain nothing from it (24.9).
+// Non-temporal: x' and h stream out to HBM.  With inputs from there 4608 x 3072 bf16
+// takes 25.9 us (4.4 TB/s) against 31.4 with stores that allocate in the caches,
+// 29484 x 1280 float32 93.8 (4.8 TB/s) against 102.4; loads of x and y gain nothing from it.
 __device__ inline void store8(uint16_t* p, const float (&f)[8]) { __builtin_nontemporal_store(pack8(f), reinterpret_cast<u32x4*>(p)); }
 __device__ inline void store8(float* p, const float (&f)[8]) {
   __builtin_nontemporal_store(f32x4{f[0], f[1], f[2], f[3]}, reinterpret_cast<f32x4*>(p));

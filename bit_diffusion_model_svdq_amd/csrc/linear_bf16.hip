@@ -24,10 +24,11 @@
 //                 wave streams its share of the channels of 16 weight rows
 //                 straight into registers.
 //
-// Measured: 4608 x 3072 -> 12288 300 us (1160 TFLOP/s) with 256 x 256 turns (with bf16
+// Measured: 4608 x 3072 -> 12288 296 us (1175 TFLOP/s) with 256 x 256 turns (with bf16
 // stored straight from the accumulators 330 us), 354 / 444 / 502 with the smaller
 // tiles; 1155 x 1288 -> 1290 with a float32 residual 14.2 us with 128 x 64, 15.9 with
-// 64 x 64, 27 with 128 x 128; 2 x 3072 -> 18432 23.7 us (4.8 TB/s) in linear_rows.
+// 64 x 64, 27 with 128 x 128, on the same inputs each time (128 x 64 with inputs from
+// HBM 18.6); 2 x 3072 -> 18432 24.7 us (4.6 TB/s) in linear_rows, 1 x 3072 -> 3072 8.5.
 #include <algorithm>
 
 #include "gemm_tail.h"

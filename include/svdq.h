@@ -40,8 +40,9 @@
  * On a validation error nothing is written.  Device functions launch work
  * asynchronously on the given stream (a hipStream_t; NULL = the null stream)
  * and do not synchronize; SVDQ_ERR_HIP reports a launch failure.  Non-finite
- * inputs are not checked: their results are undefined.  svdq_last_error()
- * returns a thread-local description of the last failure on this thread.
+ * inputs are not checked: their results are undefined where a function does not
+ * say what they are.  svdq_last_error() returns a thread-local description of
+ * the last failure on this thread.
  *
  * Ownership: the caller owns every buffer.  Host functions take host
  * pointers; device functions take device pointers.  The library allocates no
@@ -410,9 +411,10 @@ size_t svdq_attention_workspace_bytes(int64_t total_q, int64_t total_k, int batc
  * Requires head_dim a multiple of 8 up to 128 and ldk, ldv up to 2^24 (above:
  * SVDQ_ERR_UNSUPPORTED),
  * heads_q a multiple of heads_kv, scale positive and at most 2^126.  Non-finite
- * elements of K and V reach every query that sees their key (O there is not finite;
- * lse by K alone); they can also reach queries of their sequence and key head that
- * the causal mask hides them from and that see other keys, but no other sequence.
+ * elements of V make O non-finite for every query that gives their key a weight,
+ * and like those of K can reach other queries of their sequence and key head, also
+ * ones that the causal mask hides them from; but no other sequence, and no query
+ * that sees no key.
  * The sums run in an order that depends on the shapes only, so equal calls
  * give equal bits. */
 svdq_status svdq_attention_forward(const uint16_t* Q, int64_t ldq, const uint16_t* K, int64_t ldk,
