@@ -28,7 +28,8 @@ MLP up 3072 -> 12288 with GELU fused into its epilogue, MLP down
 seeded rank-16 LoRA to r = 48; the attention itself is not part of it.
 --workload dit_block_full times the whole block: the modulation linear (bf16), norm and
 modulation, those four linears, attention with 24 heads of 128 channels over the fused QKV
-output, and the two calls of gate, residual (and norm) between them.
+output, and the two calls of gate, residual (and norm) between them; a model's norm of the
+queries and keys and its rotary step are not part of it.
 """
 from __future__ import annotations
 

@@ -444,10 +444,10 @@ struct Work {
 // in flight), and everyone is done with K of tile t and V of tile t - 1, whose
 // buffers are filled again.
 //
-// Bound by the card's power: 16384 tokens x 24 x 128 take 2.98 ms (1106 TFLOP/s)
-// with 8 waves and 3.05 ms with 4, though the 4 waves' form needs 10 % fewer
-// cycles (5.3 M against 5.9 M): it moves twice the bytes from L2 and the clock
-// drops to 1.74 GHz (1.94).  MFMAs run in 59 % (53 %) of the cycles.
+// Bound by the card's power: 16384 tokens x 24 x 128 take 2.93 ms (1125 TFLOP/s)
+// with 8 waves and 2.97 ms with 4, though the 4 waves' form needs 11 % fewer
+// cycles (5.1 M against 5.7 M): it moves twice the bytes from L2 and the clock
+// drops to 1.71 GHz (1.95).  MFMAs run in 62 % (55 %) of the cycles.
 template <class H, int NW>
 __global__ __launch_bounds__(NW * 64, 2) void attention_rows(const Params p) {
   using T = Tile<H, kRows, NW>;
