@@ -54,6 +54,8 @@ EXPORTS = [
     "svdq_forward_fused", "svdq_debug_fused_forward", "svdq_forward_fused_mxfp4",
     "svdq_debug_fused_forward_mxfp4", "svdq_attention_workspace_bytes", "svdq_attention_forward",
     "svdq_block_norm_forward", "svdq_linear_bf16_workspace_bytes", "svdq_linear_bf16_forward",
+    "svdq_attention_window_workspace_bytes", "svdq_attention_window_forward",
+    "svdq_attention_prefix_workspace_bytes", "svdq_attention_prefix_forward",
 ]
 
 # svdq_activation
@@ -116,6 +118,12 @@ _sig = {
     "svdq_attention_workspace_bytes": [_L, _L, _I, _I, _I, _I],
     "svdq_attention_forward": [_P, _L, _P, _L, _P, _L, _P, _P, _I, _L, _L, _I, _I, _I, ctypes.c_float, _I, _P, _L,
                                _P, _P, ctypes.c_size_t, _P],
+    "svdq_attention_window_workspace_bytes": [_L, _L, _I, _I, _I, _I, _I, _I, _I, _I],
+    "svdq_attention_window_forward": [_P, _L, _P, _L, _P, _L, _P, _P, _I, _L, _L, _I, _I, _I, ctypes.c_float, _I, _I, _I,
+                                      _I, _P, _L, _P, _P, ctypes.c_size_t, _P],
+    "svdq_attention_prefix_workspace_bytes": [_L, _L, _L, _I, _I, _I, _I, _I],
+    "svdq_attention_prefix_forward": [_P, _L, _P, _L, _P, _L, _L, _P, _L, _P, _L, _P, _P, _I, _L, _L, _I, _I, _I,
+                                      ctypes.c_float, _I, _P, _L, _P, _P, ctypes.c_size_t, _P],
     "svdq_block_norm_forward": [_P, _I, _P, _L, _I, _P, _I, _I, _P, _P, _L, ctypes.c_float, ctypes.c_float, _I, _P, _P,
                                 _P, _L, _P, _L, ctypes.c_float, _P, _P, _P],
     "svdq_linear_bf16_workspace_bytes": [_L, _I, _I],
@@ -133,6 +141,8 @@ _lib.svdq_forward_workspace_bytes_mxfp4.restype = ctypes.c_size_t
 _lib.svdq_mxfp4_tiled_scale_bytes.restype = ctypes.c_size_t
 _lib.svdq_attention_workspace_bytes.restype = ctypes.c_size_t
 _lib.svdq_linear_bf16_workspace_bytes.restype = ctypes.c_size_t
+_lib.svdq_attention_window_workspace_bytes.restype = ctypes.c_size_t
+_lib.svdq_attention_prefix_workspace_bytes.restype = ctypes.c_size_t
 _lib.svdq_status_string.restype = ctypes.c_char_p
 _lib.svdq_last_error.restype = ctypes.c_char_p
 
@@ -712,10 +722,9 @@ def svdq_attention_workspace_bytes(total_q: int, total_k: int, batch: int, heads
     return int(_lib.svdq_attention_workspace_bytes(total_q, total_k, batch, heads_q, heads_kv, head_dim))
 
 
-def svdq_attention_forward(Q, K, V, cu_q, cu_k, scale, causal, O, lse=None, workspace=None, stream=None):
-    """O [Tq, Hq, D] (written) = attention of Q [Tq, Hq, D] over K, V [Tk, Hkv, D], bf16, for packed
-    sequences with offsets cu_q, cu_k (int32 [batch + 1] on the GPU; None: one sequence).  Rows may lie
-    apart (slices of a fused projection's output).  lse: float32 [Hq, Tq] or None."""
+def _attention_operands(Q, K, V, cu_q, cu_k, O, lse, workspace):
+    """What the attention calls share: (device index, row strides of Q, K, V, O, batch, total_q, total_k,
+    heads_q, heads_kv, head_dim)."""
     try:
         index = Q.get_device()
         ldq = _need_heads(Q, "Q")
@@ -741,9 +750,64 @@ def svdq_attention_forward(Q, K, V, cu_q, cu_k, scale, causal, O, lse=None, work
         _need_tensors(("Q", "K", "V", "O"), Q=Q, K=K, V=V, O=O, cu_q=cu_q, cu_k=cu_k, lse=lse, workspace=workspace)
         _need_cu(cu_q, "cu_q")
         raise
+    return index, ldq, ldk, ldv, ldo, batch, total_q, total_k, heads_q, heads_kv, d
+
+
+def svdq_attention_forward(Q, K, V, cu_q, cu_k, scale, causal, O, lse=None, workspace=None, stream=None):
+    """O [Tq, Hq, D] (written) = attention of Q [Tq, Hq, D] over K, V [Tk, Hkv, D], bf16, for packed
+    sequences with offsets cu_q, cu_k (int32 [batch + 1] on the GPU; None: one sequence).  Rows may lie
+    apart (slices of a fused projection's output).  lse: float32 [Hq, Tq] or None."""
+    index, ldq, ldk, ldv, ldo, batch, total_q, total_k, heads_q, heads_kv, d = _attention_operands(
+        Q, K, V, cu_q, cu_k, O, lse, workspace)
     _launch(index, stream, _lib.svdq_attention_forward, Q.data_ptr(), ldq, K.data_ptr(), ldk, V.data_ptr(), ldv,
             _ptr(cu_q), _ptr(cu_k), batch, total_q, total_k, heads_q, heads_kv, d, scale, int(causal), O.data_ptr(), ldo,
             _ptr(lse), _ptr(workspace), _bytes(workspace))
+    return O
+
+
+def svdq_attention_window_workspace_bytes(total_q: int, total_k: int, batch: int, heads_q: int, heads_kv: int,
+                                          head_dim: int, causal: bool, window_left: int, window_right: int,
+                                          sinks: int) -> int:
+    return int(_lib.svdq_attention_window_workspace_bytes(total_q, total_k, batch, heads_q, heads_kv, head_dim,
+                                                          int(causal), window_left, window_right, sinks))
+
+
+def svdq_attention_window_forward(Q, K, V, cu_q, cu_k, scale, causal, window_left, window_right, sinks, O, lse=None,
+                                  workspace=None, stream=None):
+    """svdq_attention_forward over a part of the keys: query i of nq, at key p = i + nk - nq, sees the keys
+    p - window_left .. p + window_right (-1: no limit on that side) and the first `sinks`, causal: those of
+    them up to p."""
+    index, ldq, ldk, ldv, ldo, batch, total_q, total_k, heads_q, heads_kv, d = _attention_operands(
+        Q, K, V, cu_q, cu_k, O, lse, workspace)
+    _launch(index, stream, _lib.svdq_attention_window_forward, Q.data_ptr(), ldq, K.data_ptr(), ldk, V.data_ptr(), ldv,
+            _ptr(cu_q), _ptr(cu_k), batch, total_q, total_k, heads_q, heads_kv, d, scale, int(causal), window_left,
+            window_right, sinks, O.data_ptr(), ldo, _ptr(lse), _ptr(workspace), _bytes(workspace))
+    return O
+
+
+def svdq_attention_prefix_workspace_bytes(total_q: int, prefix_len: int, total_k: int, batch: int, heads_q: int,
+                                          heads_kv: int, head_dim: int, causal: bool) -> int:
+    return int(_lib.svdq_attention_prefix_workspace_bytes(total_q, prefix_len, total_k, batch, heads_q, heads_kv,
+                                                          head_dim, int(causal)))
+
+
+def svdq_attention_prefix_forward(Q, prefix_K, prefix_V, K, V, cu_q, cu_k, scale, causal, O, lse=None, workspace=None,
+                                  stream=None):
+    """svdq_attention_forward for sequences that begin alike: every query sees all of prefix_K, prefix_V
+    [P, Hkv, D], then the keys of its own sequence in K, V (causal: those up to its own)."""
+    index, ldq, ldk, ldv, ldo, batch, total_q, total_k, heads_q, heads_kv, d = _attention_operands(
+        Q, K, V, cu_q, cu_k, O, lse, workspace)
+    try:
+        ldpk = _need_heads(prefix_K, "prefix_K", index, d, None, heads_kv)
+        prefix_len = prefix_K.shape[0]
+        ldpv = _need_heads(prefix_V, "prefix_V", index, d, prefix_len, heads_kv)
+    except AttributeError:
+        _need_tensors(("prefix_K", "prefix_V"), prefix_K=prefix_K, prefix_V=prefix_V)
+        raise
+    _launch(index, stream, _lib.svdq_attention_prefix_forward, Q.data_ptr(), ldq, prefix_K.data_ptr(), ldpk,
+            prefix_V.data_ptr(), ldpv, prefix_len, K.data_ptr(), ldk, V.data_ptr(), ldv, _ptr(cu_q), _ptr(cu_k), batch,
+            total_q, total_k, heads_q, heads_kv, d, scale, int(causal), O.data_ptr(), ldo, _ptr(lse), _ptr(workspace),
+            _bytes(workspace))
     return O
 
 

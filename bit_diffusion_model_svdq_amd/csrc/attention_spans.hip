@@ -1,0 +1,130 @@
+// svdq_attention_window_forward and svdq_attention_prefix_forward: attention over keys in
+// two pieces, first keys and a window, or a shared prefix and a sequence's own keys.  The
+// kernels are attention_core.h's with SPANS.
+#include "attention_core.h"
+
+namespace svdq {
+namespace {
+
+// Partial rows of a cut-off prefix that a call may ask its caller to hold: 8192 new tokens x 32 x 128.
+constexpr int64_t kMaxSplitBytes = int64_t(256) << 20;
+
+struct SpanPlan {
+  Plan own;               // the whole work, or with a cut-off prefix that against the own keys
+  int pre_splits = 0, pre_tiles = 0;
+  int64_t blocks = 0;     // workgroups of the launch
+  size_t part = 0, bytes = 0;
+};
+
+// Own keys that a query sees at most.
+double window_of(const SpanArgs& a) {
+  const int right = a.causal ? 0 : a.right;
+  return a.left < 0 || right < 0 ? INFINITY : (double)a.sinks + a.left + right + 1;
+}
+
+// A prefix is cut off where that is less work by the same estimate as in plan_of: new
+// tokens of several sequences, each of which would otherwise read it for itself, with most
+// of the MFMA's 32 columns idle.
+SpanPlan plan_spans(const SpanArgs& a) {
+  SpanPlan sp;
+  const int group = a.heads_q / a.heads_kv;
+  const int64_t rows = (int64_t)a.total_q * group;
+  sp.own = plan_of(a.total_q, a.total_k, a.batch, a.heads_q, a.heads_kv, a.head_dim, a.causal != 0, window_of(a),
+                   a.prefix);
+  if (a.prefix > 0 && a.batch > 1 && rows <= (int64_t)a.batch * kTokenRows) {
+    const int64_t cus = device_cu_count();
+    const Cost cost = cost_of(a.head_dim);
+    const int64_t pre_tiles = (rows + kWaveRows - 1) / kWaveRows;
+    const int64_t tiles = std::min<int64_t>(rows / kWaveRows + a.batch, rows);
+    const double mean_own = (double)a.total_k / a.batch;
+    const double keys = ((double)pre_tiles * a.prefix + (double)tiles * mean_own) * a.heads_kv;
+    const int64_t fair = (int64_t)std::min(std::ceil(keys / (2.0 * cus) / 128) * 128, (double)INT32_MAX);
+    const int chunk = (int)std::max<int64_t>(256, fair);
+    const int pre_splits = (int)std::min<int64_t>((a.prefix + (int64_t)chunk - 1) / chunk, 32);
+    const int64_t want = std::max<int64_t>(4 * cus / std::max<int64_t>(tiles * a.heads_kv, 1), 1);
+    const int splits = (int)std::max<int64_t>(std::min<int64_t>({want, (a.total_k + (int64_t)chunk - 1) / chunk, 32}), 1);
+    const double turn = 32.0 * cost.keys_waves;
+    const double longest = std::max((double)a.prefix / pre_splits, std::min(mean_own, (double)chunk));
+    const double us = std::max(std::ceil(longest / turn) * cost.keys, keys / turn / cus * cost.keys_each) + 4.0 +
+                      4.3e-6 * rows * a.heads_kv * (pre_splits + std::ceil(mean_own / chunk)) * a.head_dim;
+    const int64_t slots = rows * a.heads_kv * (pre_splits + splits);
+    if (us < sp.own.us && slots * (a.head_dim + 1) * 4 <= kMaxSplitBytes) {
+      sp.pre_splits = pre_splits;
+      sp.pre_tiles = (int)pre_tiles;
+      sp.own.keys = true;
+      sp.own.parts = 2;
+      sp.own.rows = kWaveRows;
+      sp.own.splits = splits;
+      sp.own.chunk = chunk;
+      sp.own.tiles = tiles;
+    }
+  }
+  sp.blocks = (sp.own.tiles * sp.own.splits + (int64_t)sp.pre_tiles * sp.pre_splits) * a.heads_kv;
+  if (sp.own.splits > 1 || sp.pre_splits > 0) {
+    const size_t slots = sp.pre_splits > 0 ? (size_t)rows * a.heads_kv * (sp.pre_splits + sp.own.splits)
+                                           : (size_t)sp.blocks * sp.own.rows;
+    sp.part = (slots * a.head_dim * 4 + 255) & ~size_t(255);
+    sp.bytes = sp.part + ((slots * 4 + 255) & ~size_t(255));
+  }
+  return sp;
+}
+
+template <class H>
+hipError_t launch(const SpanPlan& sp, const SpanParams& p, hipStream_t stream) {
+  const Plan& pl = sp.own;
+  const dim3 grid((unsigned)sp.blocks);
+  if (pl.keys) {
+    constexpr int kWaves = key_waves(H::DP);
+    if (pl.parts == 2)
+      hipLaunchKernelGGL((attention_keys<H, kWaves, 2, true>), grid, dim3(kWaves * 64), 0, stream, p);
+    else
+      hipLaunchKernelGGL((attention_keys<H, kWaves, 1, true>), grid, dim3(kWaves * 64), 0, stream, p);
+  } else if (pl.waves == 8) {
+    if constexpr (H::DP == 128)
+      hipLaunchKernelGGL((attention_rows<H, 8, true>), grid, dim3(512), 0, stream, p);
+  } else {
+    hipLaunchKernelGGL((attention_rows<H, 4, true>), grid, dim3(256), 0, stream, p);
+  }
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || sp.bytes == 0) return e;
+  const dim3 jgrid((unsigned)(pl.tiles * p.heads_kv * (pl.rows / 4)));
+  hipLaunchKernelGGL((attention_join<true>), jgrid, dim3(256), 0, stream, p, pl.rows);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t attention_spans_workspace(const SpanArgs& a) { return a.total_q == 0 ? 0 : plan_spans(a).bytes; }
+
+int64_t attention_spans_blocks(const SpanArgs& a) {
+  const SpanPlan sp = plan_spans(a);
+  return std::max(sp.blocks, sp.own.tiles * a.heads_kv * (sp.bytes > 0 ? sp.own.rows / 4 : 1));
+}
+
+hipError_t launch_attention_spans(const SpanArgs& a, hipStream_t stream) {
+  const SpanPlan sp = plan_spans(a);
+  SpanParams p;
+  p.Q = a.Q; p.K = a.K; p.V = a.V; p.O = a.O; p.lse = a.lse;
+  p.ldq = a.ldq; p.ldk = a.ldk; p.ldv = a.ldv; p.ldo = a.ldo;
+  p.cu_q = a.cu_q; p.cu_k = a.cu_k;
+  p.batch = a.batch; p.total_q = a.total_q; p.total_k = a.total_k;
+  p.heads_q = a.heads_q; p.heads_kv = a.heads_kv; p.group = a.heads_q / a.heads_kv;
+  p.head_dim = a.head_dim;
+  p.c = a.scale * kLog2e;
+  p.causal = a.causal;
+  p.tiles = (int)sp.own.tiles;
+  p.splits = sp.own.splits;
+  p.chunk = sp.own.chunk;
+  p.part = static_cast<float*>(a.workspace);
+  p.part_lse = sp.bytes > 0 ? reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + sp.part) : nullptr;
+  p.left = a.left; p.right = a.right; p.sinks = a.sinks;
+  p.PK = a.PK; p.PV = a.PV; p.ldpk = a.ldpk; p.ldpv = a.ldpv; p.prefix = a.prefix;
+  p.reach = (int)std::min(window_of(a) + sp.own.rows / p.group + 1, (double)INT32_MAX);
+  p.pre_splits = sp.pre_splits;
+  p.pre_tiles = sp.pre_tiles;
+  if (a.head_dim <= 64) return launch<Head<64, 4, 2>>(sp, p, stream);
+  if (a.head_dim <= 96) return launch<Head<128, 6, 3>>(sp, p, stream);
+  return launch<Head<128, 8, 4>>(sp, p, stream);
+}
+
+}  // namespace svdq

@@ -303,6 +303,64 @@ svdq_status check_align4(const void* p, const char* name) {
   return SVDQ_OK;
 }
 
+// What every attention call has besides its shape.
+svdq_status check_attention_call(const AttentionArgs& a) {
+  if (!(a.scale > 0.f) || a.scale > 0x1p126f)      // the kernels take scale log2(e)
+    return fail(SVDQ_ERR_INVALID_ARG, "scale must be positive and at most 2^126 (got %g)", (double)a.scale);
+  if (a.causal != 0 && a.causal != 1) return fail(SVDQ_ERR_INVALID_ARG, "causal must be 0 or 1 (got %d)", a.causal);
+  if (a.batch > 1 && (!a.cu_q || !a.cu_k))
+    return fail(SVDQ_ERR_INVALID_ARG, "cu_q and cu_k must not be NULL for batch=%d", a.batch);
+  const int64_t wq = (int64_t)a.heads_q * a.head_dim, wk = (int64_t)a.heads_kv * a.head_dim;
+  SVDQ_TRY(check_ld(a.ldq, wq, "ldq"));
+  SVDQ_TRY(check_ld(a.ldk, wk, "ldk"));
+  SVDQ_TRY(check_ld(a.ldv, wk, "ldv"));
+  SVDQ_TRY(check_ld(a.ldo, wq, "ldo"));
+  if (a.ldk > kAttentionMaxLd || a.ldv > kAttentionMaxLd)
+    return fail(SVDQ_ERR_UNSUPPORTED, "ldk=%lld or ldv=%lld is above 2^24", (long long)a.ldk, (long long)a.ldv);
+  SVDQ_TRY(check_ptr(a.Q, "Q", a.total_q == 0));
+  SVDQ_TRY(check_ptr(a.K, "K", a.total_k == 0 || a.total_q == 0));
+  SVDQ_TRY(check_ptr(a.V, "V", a.total_k == 0 || a.total_q == 0));
+  SVDQ_TRY(check_ptr(a.O, "O", a.total_q == 0));
+  SVDQ_TRY(check_align4(a.cu_q, "cu_q"));
+  SVDQ_TRY(check_align4(a.cu_k, "cu_k"));
+  return check_align4(a.lse, "lse");
+}
+
+svdq_status check_workspace(const void* workspace, size_t bytes, size_t need) {
+  if (need == 0) return SVDQ_OK;
+  SVDQ_TRY(check_ptr(workspace, "workspace", false));
+  if (bytes < need) return fail(SVDQ_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", need, bytes);
+  return SVDQ_OK;
+}
+
+// The shape of an attention call whose keys lie in two pieces.
+svdq_status check_spans_shape(const SpanArgs& a, int64_t total_q, int64_t total_k, int64_t prefix) {
+  if (prefix < 0 || prefix > INT32_MAX - 512)
+    return fail(SVDQ_ERR_INVALID_ARG, "the prefix' %lld keys are negative or beyond 31 bits less 512", (long long)prefix);
+  SVDQ_TRY(check_attention_shape(a.batch, total_q, total_k, a.heads_q, a.heads_kv, a.head_dim));
+  if (total_k + prefix > INT32_MAX - 512)
+    return fail(SVDQ_ERR_INVALID_ARG, "total_k=%lld and the prefix' %lld keys are beyond 31 bits less 512",
+                (long long)total_k, (long long)prefix);
+  if (a.left < -1 || a.right < -1)
+    return fail(SVDQ_ERR_INVALID_ARG, "window_left=%d and window_right=%d must be -1 or more", a.left, a.right);
+  if (a.sinks < 0) return fail(SVDQ_ERR_INVALID_ARG, "sinks must not be negative (got %d)", a.sinks);
+  if (total_q > 0 && attention_spans_blocks(a) > kMaxBlocks)
+    return fail(SVDQ_ERR_INVALID_ARG, "too many rows for one launch: total_q=%lld, heads_q=%d, batch=%d",
+                (long long)total_q, a.heads_q, a.batch);
+  return SVDQ_OK;
+}
+
+SpanArgs spans_of(int batch, int64_t total_q, int64_t total_k, int heads_q, int heads_kv, int head_dim, int causal,
+                  int left, int right, int sinks, int64_t prefix) {
+  SpanArgs a = {};
+  a.batch = batch; a.total_q = (int)total_q; a.total_k = (int)total_k;
+  a.heads_q = heads_q; a.heads_kv = heads_kv; a.head_dim = head_dim;
+  a.causal = causal;
+  a.left = left; a.right = right; a.sinks = sinks;
+  a.prefix = (int)prefix;
+  return a;
+}
+
 // ---- block norms and the 16-bit linear
 svdq_status check_dtype(int dtype, const char* name) {
   if (dtype != SVDQ_BF16 && dtype != SVDQ_F32)
@@ -537,35 +595,75 @@ svdq_status svdq_attention_forward(const uint16_t* Q, int64_t ldq, const uint16_
                                    void* workspace, size_t workspace_bytes, void* stream) {
   return guarded([&]() -> svdq_status {
     SVDQ_TRY(check_attention_shape(batch, total_q, total_k, heads_q, heads_kv, head_dim));
-    if (!(scale > 0.f) || scale > 0x1p126f)      // the kernels take scale log2(e)
-      return fail(SVDQ_ERR_INVALID_ARG, "scale must be positive and at most 2^126 (got %g)", (double)scale);
-    if (causal != 0 && causal != 1) return fail(SVDQ_ERR_INVALID_ARG, "causal must be 0 or 1 (got %d)", causal);
-    if (batch > 1 && (!cu_q || !cu_k))
-      return fail(SVDQ_ERR_INVALID_ARG, "cu_q and cu_k must not be NULL for batch=%d", batch);
-    const int64_t wq = (int64_t)heads_q * head_dim, wk = (int64_t)heads_kv * head_dim;
-    SVDQ_TRY(check_ld(ldq, wq, "ldq"));
-    SVDQ_TRY(check_ld(ldk, wk, "ldk"));
-    SVDQ_TRY(check_ld(ldv, wk, "ldv"));
-    SVDQ_TRY(check_ld(ldo, wq, "ldo"));
-    if (ldk > kAttentionMaxLd || ldv > kAttentionMaxLd)
-      return fail(SVDQ_ERR_UNSUPPORTED, "ldk=%lld or ldv=%lld is above 2^24", (long long)ldk, (long long)ldv);
-    SVDQ_TRY(check_ptr(Q, "Q", total_q == 0));
-    SVDQ_TRY(check_ptr(K, "K", total_k == 0 || total_q == 0));
-    SVDQ_TRY(check_ptr(V, "V", total_k == 0 || total_q == 0));
-    SVDQ_TRY(check_ptr(O, "O", total_q == 0));
-    SVDQ_TRY(check_align4(cu_q, "cu_q"));
-    SVDQ_TRY(check_align4(cu_k, "cu_k"));
-    SVDQ_TRY(check_align4(lse, "lse"));
+    const AttentionArgs a = {Q, K, V, ldq, ldk, ldv, ldo, cu_q, cu_k, batch, (int)total_q, (int)total_k, heads_q,
+                             heads_kv, head_dim, scale, causal, O, lse, workspace};
+    SVDQ_TRY(check_attention_call(a));
     if (total_q == 0) return SVDQ_OK;
-    AttentionArgs a = {Q, K, V, ldq, ldk, ldv, ldo, cu_q, cu_k, batch, (int)total_q, (int)total_k, heads_q,
-                       heads_kv, head_dim, scale, causal, O, lse, workspace};
-    const size_t need = attention_workspace(a.total_q, a.total_k, batch, heads_q, heads_kv, head_dim);
-    if (need > 0) {
-      SVDQ_TRY(check_ptr(workspace, "workspace", false));
-      if (workspace_bytes < need)
-        return fail(SVDQ_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", need, workspace_bytes);
-    }
+    SVDQ_TRY(check_workspace(workspace, workspace_bytes,
+                             attention_workspace(a.total_q, a.total_k, batch, heads_q, heads_kv, head_dim)));
     return hip_check(launch_attention(a, static_cast<hipStream_t>(stream)), "attention launch");
+  });
+}
+
+size_t svdq_attention_window_workspace_bytes(int64_t total_q, int64_t total_k, int batch, int heads_q, int heads_kv,
+                                             int head_dim, int causal, int window_left, int window_right, int sinks) {
+  const SpanArgs a = spans_of(batch, total_q, total_k, heads_q, heads_kv, head_dim, causal, window_left, window_right,
+                              sinks, 0);
+  return check_spans_shape(a, total_q, total_k, 0) == SVDQ_OK ? attention_spans_workspace(a) : 0;
+}
+
+svdq_status svdq_attention_window_forward(const uint16_t* Q, int64_t ldq, const uint16_t* K, int64_t ldk,
+                                          const uint16_t* V, int64_t ldv, const int32_t* cu_q, const int32_t* cu_k,
+                                          int batch, int64_t total_q, int64_t total_k, int heads_q, int heads_kv,
+                                          int head_dim, float scale, int causal, int window_left, int window_right,
+                                          int sinks, uint16_t* O, int64_t ldo, float* lse, void* workspace,
+                                          size_t workspace_bytes, void* stream) {
+  return guarded([&]() -> svdq_status {
+    SpanArgs a = spans_of(batch, total_q, total_k, heads_q, heads_kv, head_dim, causal, window_left, window_right,
+                          sinks, 0);
+    SVDQ_TRY(check_spans_shape(a, total_q, total_k, 0));
+    static_cast<AttentionArgs&>(a) = {Q, K, V, ldq, ldk, ldv, ldo, cu_q, cu_k, batch, a.total_q, a.total_k, heads_q,
+                                      heads_kv, head_dim, scale, causal, O, lse, workspace};
+    SVDQ_TRY(check_attention_call(a));
+    if (total_q == 0) return SVDQ_OK;
+    SVDQ_TRY(check_workspace(workspace, workspace_bytes, attention_spans_workspace(a)));
+    return hip_check(launch_attention_spans(a, static_cast<hipStream_t>(stream)), "attention_window launch");
+  });
+}
+
+size_t svdq_attention_prefix_workspace_bytes(int64_t total_q, int64_t prefix_len, int64_t total_k, int batch,
+                                             int heads_q, int heads_kv, int head_dim, int causal) {
+  const SpanArgs a = spans_of(batch, total_q, total_k, heads_q, heads_kv, head_dim, causal, -1, -1, 0, prefix_len);
+  return check_spans_shape(a, total_q, total_k, prefix_len) == SVDQ_OK ? attention_spans_workspace(a) : 0;
+}
+
+svdq_status svdq_attention_prefix_forward(const uint16_t* Q, int64_t ldq, const uint16_t* prefix_K, int64_t ldpk,
+                                          const uint16_t* prefix_V, int64_t ldpv, int64_t prefix_len,
+                                          const uint16_t* K, int64_t ldk, const uint16_t* V, int64_t ldv,
+                                          const int32_t* cu_q, const int32_t* cu_k, int batch, int64_t total_q,
+                                          int64_t total_k, int heads_q, int heads_kv, int head_dim, float scale,
+                                          int causal, uint16_t* O, int64_t ldo, float* lse, void* workspace,
+                                          size_t workspace_bytes, void* stream) {
+  return guarded([&]() -> svdq_status {
+    SpanArgs a = spans_of(batch, total_q, total_k, heads_q, heads_kv, head_dim, causal, -1, -1, 0, prefix_len);
+    SVDQ_TRY(check_spans_shape(a, total_q, total_k, prefix_len));
+    static_cast<AttentionArgs&>(a) = {Q, K, V, ldq, ldk, ldv, ldo, cu_q, cu_k, batch, a.total_q, a.total_k, heads_q,
+                                      heads_kv, head_dim, scale, causal, O, lse, workspace};
+    SVDQ_TRY(check_attention_call(a));
+    const int64_t wk = (int64_t)heads_kv * head_dim;
+    SVDQ_TRY(check_ld(ldpk, wk, "ldpk"));
+    SVDQ_TRY(check_ld(ldpv, wk, "ldpv"));
+    if (ldpk > kAttentionMaxLd || ldpv > kAttentionMaxLd)
+      return fail(SVDQ_ERR_UNSUPPORTED, "ldpk=%lld or ldpv=%lld is above 2^24", (long long)ldpk, (long long)ldpv);
+    SVDQ_TRY(check_ptr(prefix_K, "prefix_K", prefix_len == 0 || total_q == 0));
+    SVDQ_TRY(check_ptr(prefix_V, "prefix_V", prefix_len == 0 || total_q == 0));
+    if (total_q == 0) return SVDQ_OK;
+    a.PK = prefix_K;
+    a.PV = prefix_V;
+    a.ldpk = ldpk;
+    a.ldpv = ldpv;
+    SVDQ_TRY(check_workspace(workspace, workspace_bytes, attention_spans_workspace(a)));
+    return hip_check(launch_attention_spans(a, static_cast<hipStream_t>(stream)), "attention_prefix launch");
   });
 }
 

@@ -169,6 +169,19 @@ size_t attention_workspace(int total_q, int total_k, int batch, int heads_q, int
 int64_t attention_blocks(int total_q, int total_k, int batch, int heads_q, int heads_kv, int head_dim);
 hipError_t launch_attention(const AttentionArgs& a, hipStream_t stream);
 
+// The same over keys in two pieces (svdq_attention_window_forward, svdq_attention_prefix_forward):
+// a window of each query with first keys that stay visible, or keys that all
+// sequences share in front of their own (one of the two: prefix > 0 has no window).
+struct SpanArgs : AttentionArgs {
+  int left, right, sinks;          // -1: unlimited
+  const uint16_t *PK, *PV;
+  int64_t ldpk, ldpv;
+  int prefix;
+};
+size_t attention_spans_workspace(const SpanArgs& a);     // from the sizes, causal and the window alone
+int64_t attention_spans_blocks(const SpanArgs& a);
+hipError_t launch_attention_spans(const SpanArgs& a, hipStream_t stream);
+
 // Norms (the values of svdq_norm) and svdq_block_norm_forward's operands; NULL
 // where absent, row strides of the per-sequence vectors in elements.
 constexpr int kNormNone = 0;

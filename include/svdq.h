@@ -424,6 +424,46 @@ svdq_status svdq_attention_forward(const uint16_t* Q, int64_t ldq, const uint16_
                                    uint16_t* O, int64_t ldo, float* lse, void* workspace,
                                    size_t workspace_bytes, void* stream);
 
+/* svdq_attention_forward over a part of the keys: a window around each query and
+ * first keys that stay visible.  Query i of nq stands at key p = i + nk - nq (the
+ * last query at the last key) and sees key j where
+ *   (p - window_left <= j <= p + window_right  or  j < sinks)  and  (not causal  or  j <= p).
+ * window_left, window_right: -1 for no limit on that side, else 0 or more; sinks: 0 or
+ * more (more than there are keys: all).  Everything else is svdq_attention_forward's, with
+ * this about non-finite K and V: what lies in front of all the windows of 32 (calls with
+ * few rows) to 256 rows that are worked on together and behind the sinks, or behind all of
+ * their keys, is not read (keys that a rolling cache has given up may hold
+ * anything).  Keys between, which some of those queries see and others do not, can reach
+ * all of them. */
+size_t svdq_attention_window_workspace_bytes(int64_t total_q, int64_t total_k, int batch, int heads_q,
+                                             int heads_kv, int head_dim, int causal, int window_left,
+                                             int window_right, int sinks);
+svdq_status svdq_attention_window_forward(const uint16_t* Q, int64_t ldq, const uint16_t* K, int64_t ldk,
+                                          const uint16_t* V, int64_t ldv, const int32_t* cu_q,
+                                          const int32_t* cu_k, int batch, int64_t total_q,
+                                          int64_t total_k, int heads_q, int heads_kv, int head_dim,
+                                          float scale, int causal, int window_left, int window_right,
+                                          int sinks, uint16_t* O, int64_t ldo, float* lse,
+                                          void* workspace, size_t workspace_bytes, void* stream);
+
+/* svdq_attention_forward for sequences that begin alike: every query sees the prefix_len
+ * keys of prefix_K, prefix_V [prefix_len, heads_kv, head_dim] (rows ldpk, ldpv elements
+ * apart, as ldk and ldv), then the keys of its own sequence (causal: those up to its
+ * own, as there).  One softmax over both; the prefix is stored once, and calls of few rows
+ * per sequence also read and compute it once for all of them.  Everything else is
+ * svdq_attention_forward's; either of the two pieces may be empty, also for some
+ * of the sequences.  prefix_len + total_k: at most 2^31 - 513. */
+size_t svdq_attention_prefix_workspace_bytes(int64_t total_q, int64_t prefix_len, int64_t total_k, int batch,
+                                             int heads_q, int heads_kv, int head_dim, int causal);
+svdq_status svdq_attention_prefix_forward(const uint16_t* Q, int64_t ldq, const uint16_t* prefix_K,
+                                          int64_t ldpk, const uint16_t* prefix_V, int64_t ldpv,
+                                          int64_t prefix_len, const uint16_t* K, int64_t ldk,
+                                          const uint16_t* V, int64_t ldv, const int32_t* cu_q,
+                                          const int32_t* cu_k, int batch, int64_t total_q,
+                                          int64_t total_k, int heads_q, int heads_kv, int head_dim,
+                                          float scale, int causal, uint16_t* O, int64_t ldo, float* lse,
+                                          void* workspace, size_t workspace_bytes, void* stream);
+
 /* Types of a residual stream and of svdq_linear_bf16_forward's output. */
 typedef enum { SVDQ_BF16 = 0, SVDQ_F32 = 1 } svdq_dtype;
 

@@ -38,6 +38,51 @@ def attention(Q, K, V, cu_q, cu_k, scale, causal):
     return O, lse, A
 
 
+def sees(nq, nk, causal, left=-1, right=-1, sinks=0):
+    """bool [nq, nk]: query i, at key p = i + nk - nq, sees key j in [p - left, p + right] (-1: no
+    limit) or among the first `sinks`; causal: none past p."""
+    p = np.arange(nq)[:, None] + nk - nq
+    j = np.arange(nk)[None, :]
+    window = np.ones((nq, nk), bool)
+    if left >= 0:
+        window &= j >= p - left
+    if right >= 0:
+        window &= j <= p + right
+    window |= j < sinks
+    return window & (j <= p) if causal else window
+
+
+def attention_spans(Q, K, V, cu_q, cu_k, scale, causal, left=-1, right=-1, sinks=0, PK=None, PV=None):
+    """attention() over a window and first keys, and over keys PK, PV [P, Hkv, D] that every query
+    sees: (O, lse, A) as there, and M [Hq, Tq] = max_j sum_d |q_d k_d| over the keys that are seen."""
+    Tq, Hq, D = Q.shape
+    G = Hq // K.shape[1]
+    O, A = np.full(Q.shape, np.nan), np.full(Q.shape, np.nan)
+    lse, M = np.full((Hq, Tq), np.nan), np.zeros((Hq, Tq))
+    for b in range(len(cu_q) - 1):
+        q0, q1, k0, k1 = cu_q[b], cu_q[b + 1], cu_k[b], cu_k[b + 1]
+        if q1 == q0:
+            continue
+        own = sees(q1 - q0, k1 - k0, causal, left, right, sinks)
+        for h in range(Hq):
+            q, k, v, seen = Q[q0:q1, h], K[k0:k1, h // G], V[k0:k1, h // G], own
+            if PK is not None:
+                k, v = np.concatenate([PK[:, h // G], k]), np.concatenate([PV[:, h // G], v])
+                seen = np.concatenate([np.ones((q1 - q0, len(PK)), bool), own], axis=1)
+            used = seen.any(axis=0)              # what no query sees may hold anything
+            k, v, seen = k[used], v[used], seen[:, used]
+            s = np.where(seen, scale * (q @ k.T), -np.inf)
+            m = s.max(axis=1, initial=-np.inf)
+            e = np.exp(s - np.where(np.isfinite(m), m, 0.0)[:, None])
+            l = e.sum(axis=1)
+            p = e / np.where(l > 0, l, 1.0)[:, None]
+            O[q0:q1, h], A[q0:q1, h] = p @ v, p @ np.abs(v)
+            with np.errstate(divide="ignore"):
+                lse[h, q0:q1] = m + np.log(l)
+            M[h, q0:q1] = np.where(seen, np.abs(q) @ np.abs(k).T, 0.0).max(axis=1, initial=0.0)
+    return O, lse, A, M
+
+
 def _norm(v, kind, eps):
     if kind == "none":
         return v
