@@ -55,7 +55,7 @@ EXPORTS = [
     "svdq_debug_fused_forward_mxfp4", "svdq_attention_workspace_bytes", "svdq_attention_forward",
     "svdq_block_norm_forward", "svdq_linear_bf16_workspace_bytes", "svdq_linear_bf16_forward",
     "svdq_attention_window_workspace_bytes", "svdq_attention_window_forward",
-    "svdq_attention_prefix_workspace_bytes", "svdq_attention_prefix_forward",
+    "svdq_attention_prefix_workspace_bytes", "svdq_attention_prefix_forward", "svdq_qk_norm_rope_forward",
 ]
 
 # svdq_activation
@@ -66,6 +66,9 @@ SVDQ_ACT_SILU = 2               # svdq_linear_bf16_forward only
 # svdq_norm, svdq_dtype
 SVDQ_NORM_NONE, SVDQ_NORM_RMS, SVDQ_NORM_LAYER = 0, 1, 2
 SVDQ_BF16, SVDQ_F32 = 0, 1
+
+# svdq_rope_pairs
+SVDQ_ROPE_NEIGHBOURS, SVDQ_ROPE_HALVES = 0, 1
 
 
 class SvdqError(RuntimeError):
@@ -124,6 +127,8 @@ _sig = {
     "svdq_attention_prefix_workspace_bytes": [_L, _L, _L, _I, _I, _I, _I, _I],
     "svdq_attention_prefix_forward": [_P, _L, _P, _L, _P, _L, _L, _P, _L, _P, _L, _P, _P, _I, _L, _L, _I, _I, _I,
                                       ctypes.c_float, _I, _P, _L, _P, _P, ctypes.c_size_t, _P],
+    "svdq_qk_norm_rope_forward": [_P, _L, _P, _L, _L, _I, _I, _I, _P, _I, _P, _I, _P, _P, _P, _P, ctypes.c_float, _P, _P,
+                                  _L, _L, _I, _I, _P, _L, _P, _L, _P],
     "svdq_block_norm_forward": [_P, _I, _P, _L, _I, _P, _I, _I, _P, _P, _L, ctypes.c_float, ctypes.c_float, _I, _P, _P,
                                 _P, _L, _P, _L, ctypes.c_float, _P, _P, _P],
     "svdq_linear_bf16_workspace_bytes": [_L, _I, _I],
@@ -866,6 +871,72 @@ def svdq_block_norm_forward(x, y, cu, post, post_weight, gate, residual_scale, b
             width, _ptr(cu), batch, post, _ptr(post_weight), _ptr(gate), ld_gate, residual_scale, branch_scale, pre,
             _ptr(pre_weight), _ptr(pre_bias), _ptr(scale), ld_scale, _ptr(shift), ld_shift, eps, _ptr(x_out), _ptr(h))
     return x_out, h
+
+
+def _need_table(cos, sin, index):
+    """(row stride, rows, rotary_dim) of a rotation's tables, float32 [positions, rotary_dim / 2] alike on
+    device `index`, whose rows may lie apart."""
+    shape, strides = cos.shape, cos.stride()
+    if cos.get_device() != index or sin.get_device() != index:
+        raise ValueError(f"tensors live on different devices: cos on {cos.device}, sin on {sin.device}")
+    if cos.dtype not in _T_F32 or sin.dtype not in _T_F32:
+        raise ValueError(f"cos and sin must have dtype float32 (got {_dtype_name(cos)} and {_dtype_name(sin)})")
+    if len(shape) != 2 or sin.shape != shape:
+        raise ValueError(f"cos and sin must be [positions, rotary_dim / 2] alike (got {tuple(shape)} and {tuple(sin.shape)})")
+    rows, pairs = shape
+    if (pairs > 1 and (strides[1] != 1 or sin.stride(1) != 1)) or (rows > 1 and sin.stride(0) != strides[0]):
+        raise ValueError(f"cos and sin: the angles of a position must be contiguous, the rows alike (strides {strides}, "
+                         f"{sin.stride()})")
+    return (strides[0] if rows > 1 else -(-pairs // 4) * 4), rows, 2 * pairs
+
+
+def svdq_qk_norm_rope_forward(Q, K, cu, positions, norm, q_weight, q_bias, k_weight, k_bias, eps, cos, sin, pairs, Q_out,
+                              K_out, stream=None):
+    """Q_out, K_out (written) = the heads of Q [rows, Hq, D] and K [rows, Hk, D], bf16, normalised (norm:
+    SVDQ_NORM_*, weight and bias [D] or None) and their first channels turned by the position: cos, sin
+    float32 [positions, rotary_dim / 2] (None: not turned), pairs: SVDQ_ROPE_*.  positions: int32 [rows], or
+    None for a token's number in its sequence (cu: int32 [batch + 1] offsets, None for one sequence); one
+    outside of the table turns nothing.  Rows may lie apart; Q_out may be Q and K_out K; Q or K may be None
+    with all that is theirs."""
+    try:
+        first = K if Q is None else Q
+        if first is None:
+            raise ValueError("Q and K are both None")
+        index = first.get_device()
+        ldq = ldk = ldqo = ldko = heads_q = heads_k = 0
+        if Q is not None:
+            ldq = _need_heads(Q, "Q")
+            rows, heads_q, d = Q.shape
+            ldqo = _need_heads(Q_out, "Q_out", index, d, rows, heads_q)
+        if K is not None:
+            if Q is None:
+                ldk = _need_heads(K, "K")
+                rows, heads_k, d = K.shape
+            else:
+                ldk = _need_heads(K, "K", index, d, rows)
+                heads_k = K.shape[1]
+            ldko = _need_heads(K_out, "K_out", index, d, rows, heads_k)
+        batch = 1 if cu is None else cu.shape[0] - 1
+        if not (_agree(index, (cu, _T_I32, (batch + 1,)), (positions, _T_I32, (rows,)), (q_weight, _T_BF16, (d,)),
+                       (q_bias, _T_BF16, (d,)), (k_weight, _T_BF16, (d,)), (k_bias, _T_BF16, (d,))) and batch >= 1):
+            batch = _need_cu(cu, "cu")
+            _need(positions, "positions", ("int32",), (rows,), optional=True)
+            for t, name in ((q_weight, "q_weight"), (q_bias, "q_bias"), (k_weight, "k_weight"), (k_bias, "k_bias")):
+                _need(t, name, _BF16, (d,), optional=True)
+            _same_device(first, cu, positions, q_weight, q_bias, k_weight, k_bias)
+        if (cos is None) != (sin is None):
+            raise ValueError("cos and sin must both be given (or both None)")
+        ldt, table_rows, rotary_dim = (0, 0, 0) if cos is None else _need_table(cos, sin, index)
+    except (AttributeError, IndexError):
+        names = ((("Q", "Q_out") if Q is not None else ()) + (("K", "K_out") if K is not None else ()))
+        _need_tensors(names, Q=Q, K=K, cu=cu, positions=positions, q_weight=q_weight, q_bias=q_bias, k_weight=k_weight,
+                      k_bias=k_bias, cos=cos, sin=sin, Q_out=Q_out, K_out=K_out)
+        _need_cu(cu, "cu")
+        raise
+    _launch(index, stream, _lib.svdq_qk_norm_rope_forward, _ptr(Q), ldq, _ptr(K), ldk, rows, heads_q, heads_k, d,
+            _ptr(cu), batch, _ptr(positions), norm, _ptr(q_weight), _ptr(q_bias), _ptr(k_weight), _ptr(k_bias), eps,
+            _ptr(cos), _ptr(sin), ldt, table_rows, rotary_dim, pairs, _ptr(Q_out), ldqo, _ptr(K_out), ldko)
+    return Q_out, K_out
 
 
 def svdq_linear_bf16_workspace_bytes(M: int, K: int, N: int) -> int:

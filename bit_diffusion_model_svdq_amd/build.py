@@ -32,7 +32,8 @@ CXX_FLAGS = ["-O3", "-std=c++17", "-fPIC", "-ffp-contract=off", "-fopenmp",
 
 HIP_SOURCES = ["svdq_api.hip", "k1_smooth_quant.hip", "k2_w4a4_gemm.hip", "k2_mxfp4_gemm.hip",
                "calib_absmax.hip", "k12_fused_smallk.hip", "attention.hip", "block_norm.hip",
-               "linear_bf16.hip", "attention_spans.hip"]
+               "linear_bf16.hip", "attention_spans.hip",
+               "qk_norm_rope.hip"]
 CXX_SOURCES = ["pack.cpp"]
 
 

@@ -268,6 +268,8 @@ svdq_status linear_forward_mx(const uint16_t* X, int M, int K, int N, int r, con
 // Most workgroups of a launch: the runtime takes fewer than 2^32 work-items,
 // and no kernel here has more than 512 per workgroup.
 constexpr int64_t kMaxBlocks = (int64_t(1) << 23) - 1;
+// Heads that svdq_qk_norm_rope_forward counts in 32 bits, with their steps.
+constexpr int kMaxHeads = 1 << 20;
 
 svdq_status check_attention_shape(int batch, int64_t total_q, int64_t total_k, int heads_q, int heads_kv,
                                   int head_dim) {
@@ -714,6 +716,77 @@ svdq_status svdq_block_norm_forward(const void* x, int stream_dtype, const uint1
                              h};
     return hip_check(launch_block_norm(a, stream_dtype == SVDQ_F32, static_cast<hipStream_t>(stream)),
                      "block_norm launch");
+  });
+}
+
+svdq_status svdq_qk_norm_rope_forward(const uint16_t* Q, int64_t ldq, const uint16_t* K, int64_t ldk, int64_t rows,
+                                      int heads_q, int heads_k, int head_dim, const int32_t* cu, int batch,
+                                      const int32_t* positions, int norm, const uint16_t* q_weight,
+                                      const uint16_t* q_bias, const uint16_t* k_weight, const uint16_t* k_bias,
+                                      float eps, const float* cos, const float* sin, int64_t ld_table,
+                                      int64_t table_rows, int rotary_dim, int pairs, uint16_t* Q_out, int64_t ldqo,
+                                      uint16_t* K_out, int64_t ldko, void* stream) {
+  return guarded([&]() -> svdq_status {
+    if (rows < 0 || rows > INT32_MAX)      // positions and offsets are 32-bit numbers
+      return fail(SVDQ_ERR_INVALID_ARG, "rows=%lld is negative or beyond 31 bits", (long long)rows);
+    if (heads_q < 0 || heads_k < 0 || (heads_q == 0 && heads_k == 0) || heads_q > kMaxHeads || heads_k > kMaxHeads)
+      return fail(SVDQ_ERR_INVALID_ARG, "heads_q=%d and heads_k=%d must be 0 to %d, one of them at least 1", heads_q,
+                  heads_k, kMaxHeads);
+    if (head_dim < 8 || head_dim % 8)
+      return fail(SVDQ_ERR_INVALID_ARG, "head_dim must be a positive multiple of 8 (got %d)", head_dim);
+    if (head_dim > kMaxRopeHead) return fail(SVDQ_ERR_UNSUPPORTED, "head_dim %d is above %d", head_dim, kMaxRopeHead);
+    if (batch < 1) return fail(SVDQ_ERR_INVALID_ARG, "batch must be >= 1 (got %d)", batch);
+    if (batch > 1 && !cu) return fail(SVDQ_ERR_INVALID_ARG, "cu must not be NULL for batch=%d", batch);
+    SVDQ_TRY(check_norm(norm, "norm"));
+    if (!(eps >= 0.f) || !isfinite(eps))
+      return fail(SVDQ_ERR_INVALID_ARG, "eps must be finite and not negative (got %g)", (double)eps);
+    if (rotary_dim < 0 || rotary_dim % 8 || rotary_dim > head_dim)
+      return fail(SVDQ_ERR_INVALID_ARG, "rotary_dim must be a multiple of 8 in [0, head_dim] (got %d)", rotary_dim);
+    if (pairs != SVDQ_ROPE_NEIGHBOURS && pairs != SVDQ_ROPE_HALVES)
+      return fail(SVDQ_ERR_INVALID_ARG, "pairs %d is not one of svdq_rope_pairs", pairs);
+    if (rotary_dim > 0) {
+      if (table_rows < 0 || ld_table < rotary_dim / 2 || ld_table % 4)
+        return fail(SVDQ_ERR_INVALID_ARG,
+                    "table_rows=%lld must not be negative, and ld_table=%lld a multiple of 4 and at least %d",
+                    (long long)table_rows, (long long)ld_table, rotary_dim / 2);
+      SVDQ_TRY(check_ptr(cos, "cos", rows == 0 || table_rows == 0));
+      SVDQ_TRY(check_ptr(sin, "sin", rows == 0 || table_rows == 0));
+    } else if (cos || sin) {
+      return fail(SVDQ_ERR_INVALID_ARG, "cos and sin must be NULL without a rotary_dim");
+    }
+    const int64_t wq = (int64_t)heads_q * head_dim, wk = (int64_t)heads_k * head_dim;
+    if (heads_q > 0) {
+      SVDQ_TRY(check_ld(ldq, wq, "ldq"));
+      SVDQ_TRY(check_ld(ldqo, wq, "ldqo"));
+      if (Q == Q_out && ldq != ldqo) return fail(SVDQ_ERR_INVALID_ARG, "Q_out is Q with another row stride");
+      SVDQ_TRY(check_ptr(Q, "Q", rows == 0));
+      SVDQ_TRY(check_ptr(Q_out, "Q_out", rows == 0));
+    } else if (Q || Q_out || q_weight || q_bias) {
+      return fail(SVDQ_ERR_INVALID_ARG, "heads_q=0 with a Q operand");
+    }
+    if (heads_k > 0) {
+      SVDQ_TRY(check_ld(ldk, wk, "ldk"));
+      SVDQ_TRY(check_ld(ldko, wk, "ldko"));
+      if (K == K_out && ldk != ldko) return fail(SVDQ_ERR_INVALID_ARG, "K_out is K with another row stride");
+      SVDQ_TRY(check_ptr(K, "K", rows == 0));
+      SVDQ_TRY(check_ptr(K_out, "K_out", rows == 0));
+    } else if (K || K_out || k_weight || k_bias) {
+      return fail(SVDQ_ERR_INVALID_ARG, "heads_k=0 with a K operand");
+    }
+    SVDQ_TRY(check_ptr(q_weight, "q_weight", true));
+    SVDQ_TRY(check_ptr(q_bias, "q_bias", true));
+    SVDQ_TRY(check_ptr(k_weight, "k_weight", true));
+    SVDQ_TRY(check_ptr(k_bias, "k_bias", true));
+    SVDQ_TRY(check_align4(cu, "cu"));
+    SVDQ_TRY(check_align4(positions, "positions"));
+    if (rows == 0) return SVDQ_OK;
+    const QkNormRopeArgs a = {Q, K, ldq, ldk, rows, heads_q, heads_k, head_dim, cu, batch, positions, norm, q_weight,
+                              q_bias, k_weight, k_bias, eps, cos, sin, ld_table, table_rows, rotary_dim,
+                              pairs == SVDQ_ROPE_HALVES, Q_out, ldqo, K_out, ldko};
+    if (qk_norm_rope_blocks(a) > kMaxBlocks)
+      return fail(SVDQ_ERR_INVALID_ARG, "too many rows for one launch: rows=%lld, heads_q=%d, heads_k=%d",
+                  (long long)rows, heads_q, heads_k);
+    return hip_check(launch_qk_norm_rope(a, static_cast<hipStream_t>(stream)), "qk_norm_rope launch");
   });
 }
 

@@ -213,6 +213,31 @@ struct BlockNormArgs {
 // fp32: the type of x and x_out (else bf16).
 hipError_t launch_block_norm(const BlockNormArgs& a, bool fp32, hipStream_t stream);
 
+// svdq_qk_norm_rope_forward's operands; NULL where absent.
+constexpr int kMaxRopeHead = 256;
+struct QkNormRopeArgs {
+  const uint16_t *Q, *K;
+  int64_t ldq, ldk;
+  int64_t rows;
+  int heads_q, heads_k, head_dim;
+  const int32_t* cu;
+  int batch;
+  const int32_t* positions;
+  int norm;
+  const uint16_t *q_weight, *q_bias, *k_weight, *k_bias;
+  float eps;
+  const float *cos, *sin;
+  int64_t ld_table, table_rows;
+  int rotary_dim;
+  bool halves;
+  uint16_t* Q_out;
+  int64_t ldqo;
+  uint16_t* K_out;
+  int64_t ldko;
+};
+int64_t qk_norm_rope_blocks(const QkNormRopeArgs& a);      // workgroups of its launch
+hipError_t launch_qk_norm_rope(const QkNormRopeArgs& a, hipStream_t stream);
+
 // The 16-bit linear Y = act(X W^T + bias) + residual; Y and the residual float32
 // (fp32) or bf16.  The caller fills the first line and part (the workspace,
 // linear_workspace() bytes).

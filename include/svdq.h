@@ -495,6 +495,35 @@ svdq_status svdq_block_norm_forward(const void* x, int stream_dtype, const uint1
                                     int64_t ld_shift, float eps, void* x_out, uint16_t* h,
                                     void* stream);
 
+/* Which channels of a head's first rotary_dim = r are turned together:
+ * (2 i, 2 i + 1), or (i, i + r / 2). */
+typedef enum { SVDQ_ROPE_NEIGHBOURS = 0, SVDQ_ROPE_HALVES = 1 } svdq_rope_pairs;
+
+/* What stands between the QKV projection and attention: the norm of each head of the
+ * queries and keys, and its rotation by the token's position, in one pass:
+ *   n = norm(v) weight + bias                     over the head_dim channels of a head
+ *   x' = x cos[p, i] - y sin[p, i],  y' = y cos[p, i] + x sin[p, i]
+ * for the pairs (x, y) of n's first rotary_dim channels; in float32, rounded once.
+ *   Q [rows, heads_q, head_dim], K [rows, heads_k, head_dim] bf16, rows ldq, ldk elements
+ *   apart (multiples of 8: column slices of one projection's output), outputs likewise.
+ *   Either may be absent: its heads 0 and its pointers NULL.  Q_out may be Q and K_out K (with
+ *   the same row stride); otherwise outputs must not overlap inputs or each other.
+ *   norm: an svdq_norm.  q_weight, q_bias, k_weight, k_bias: bf16 [head_dim], each may be NULL.
+ *   cos, sin: float32 [table_rows, rotary_dim / 2], rows ld_table elements apart (a
+ *   multiple of 4); NULL with rotary_dim 0 for no rotation.
+ *   positions: int32 [rows], or NULL: a token's number in its sequence.  A position
+ *   outside of [0, table_rows) turns nothing (tokens without a place).
+ * rotary_dim: a multiple of 8 up to head_dim; head_dim: a multiple of 8 up to 256 (above:
+ * SVDQ_ERR_UNSUPPORTED).  Packed sequences as above (cu, batch). */
+svdq_status svdq_qk_norm_rope_forward(const uint16_t* Q, int64_t ldq, const uint16_t* K, int64_t ldk,
+                                      int64_t rows, int heads_q, int heads_k, int head_dim,
+                                      const int32_t* cu, int batch, const int32_t* positions, int norm,
+                                      const uint16_t* q_weight, const uint16_t* q_bias,
+                                      const uint16_t* k_weight, const uint16_t* k_bias, float eps,
+                                      const float* cos, const float* sin, int64_t ld_table,
+                                      int64_t table_rows, int rotary_dim, int pairs, uint16_t* Q_out,
+                                      int64_t ldqo, uint16_t* K_out, int64_t ldko, void* stream);
+
 /* Workspace of svdq_linear_bf16_forward in bytes (float32 sums where the
  * channels are cut into shares; depends on the current device's compute-unit
  * count).  0: none is needed, or the shape is rejected. */

@@ -120,6 +120,35 @@ def block_norm(x, y, cu, post, w_post, gate, a, c, pre, w_pre, b_pre, scale, shi
     return xo, h
 
 
+def qk_norm_rope(v, cu, positions, kind, w, bias, eps, cos, sin, halves):
+    """One of Q, K [rows, H, D] in float64: (turned, n, pairs' cosines and sines [rows, 1, r / 2]); n the
+    normalised values before weight and bias.  positions None: a token's number in its sequence; one outside
+    of the tables [positions, r / 2] turns nothing.  Rows outside the sequences: NaN."""
+    rows, H, D = v.shape
+    n = _norm(v.reshape(rows * H, D), kind, eps).reshape(v.shape)
+    t = n * (1.0 if w is None else w) + (0.0 if bias is None else bias)
+    at = np.full(rows, -1, np.int64)
+    for b in range(len(cu) - 1):
+        at[cu[b]:cu[b + 1]] = np.arange(cu[b + 1] - cu[b]) if positions is None else positions[cu[b]:cu[b + 1]]
+    r = 0 if cos is None else 2 * cos.shape[1]
+    c, s = np.ones((rows, 1, r // 2)), np.zeros((rows, 1, r // 2))
+    if r:
+        known = (at >= 0) & (at < len(cos))
+        c[known, 0], s[known, 0] = cos[at[known]], sin[at[known]]
+    out = t.copy()
+    first, second = pairs_of(r, halves)
+    out[..., first] = t[..., first] * c - t[..., second] * s
+    out[..., second] = t[..., second] * c + t[..., first] * s
+    out[:cu[0]], out[cu[-1]:] = np.nan, np.nan
+    return out, n, c, s
+
+
+def pairs_of(r, halves):
+    """The channels of the pairs' first and second members."""
+    i = np.arange(r // 2)
+    return (i, i + r // 2) if halves else (2 * i, 2 * i + 1)
+
+
 def activation(z, act):
     if act == "gelu":
         return 0.5 * z * (1 + np.tanh(np.sqrt(2 / np.pi) * (z + 0.044715 * z**3)))
