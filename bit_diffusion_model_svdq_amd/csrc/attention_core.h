@@ -114,25 +114,26 @@ struct SpanParams : Params {
   int64_t ldpk, ldpv;
   int prefix;            // shared keys; 0 with a window or sinks
   int reach;             // own keys that a tile sees at most (sinks and window), for the shares
-  int pre_splits, pre_tiles;   // shares of the cut-off prefix and tiles of all rows; the launch's first workgroups
+  int pre_splits, pre_tiles, pre_blocks;   // shares of the cut-off prefix, tiles of all rows; the launch's first workgroups
+  Quotient by_heads, by_group, by_tiles, by_pre_tiles;
 
   __device__ int keys(int nk) const { return min(nk, reach) + (pre_splits > 0 ? 0 : prefix); }
-  __device__ int pre_blocks() const { return pre_splits * pre_tiles * heads_kv; }
   // With a cut-off prefix, the partial row of share s (its shares first) of a query's row:
   // rows of sequences that fill little of their tiles take no more room for it.
   __device__ int64_t slot(int s, int hk, int query, int in_group) const {
     return ((int64_t)s * heads_kv + hk) * total_q * group + (int64_t)query * group + in_group;
   }
-  // Query `token` of nq against nk own keys sees [lo, hi) and [0, first).
+  // Query `token` of nq against nk own keys sees [lo, hi) and [0, first).  left and right may
+  // be anything up to 2^31 - 1: the sums are ordered so that none leaves 32 bits.
   __device__ void view(int token, int nq, int nk, int& lo, int& hi, int& first) const {
-    const int64_t at = (int64_t)token + nk - nq;
-    auto within = [&](int64_t v) { return (int)min(max(v, (int64_t)0), (int64_t)nk); };
-    lo = left < 0 ? 0 : within(at - left);
-    hi = right < 0 ? nk : within(at + right + 1);
+    const int behind = nq - token;                     // at least 1: the query stands at key nk - behind
+    const int at = max(nk - behind, -1);
+    lo = left < 0 ? 0 : max(at - left, 0);
+    hi = right < 0 ? nk : max(nk - max(behind - 1 - right, 0), 0);
     first = min(sinks, nk);
     if (causal) {
-      hi = min(hi, within(at + 1));
-      first = min(first, within(at + 1));
+      hi = min(hi, at + 1);
+      first = min(first, at + 1);
     }
   }
   __device__ bool sees(int token, int nq, int nk) const {
@@ -205,6 +206,13 @@ __device__ inline void span(const int32_t* cu, int b, int total, int& begin, int
   len = max(min(hi, total) - begin, 0);
 }
 
+// span() of one sequence, known to be the same in all lanes.
+__device__ inline void span_uniform(const int32_t* cu, int b, int total, int& begin, int& len) {
+  span(cu, b, total, begin, len);
+  begin = __builtin_amdgcn_readfirstlane(begin);
+  len = __builtin_amdgcn_readfirstlane(len);
+}
+
 // Where a tile lies: its number in its sequence, and the sequence's rows.
 struct Place {
   int local, q0, nq, kv0, nk;
@@ -227,6 +235,48 @@ __device__ inline bool find_tile(const Params& p, int rows, int t, int lane, Pla
         if (lane >= s) end += o;
       }
     }
+    const uint64_t after = __ballot(t < end);
+    if (after) {
+      const int l = __builtin_ctzll(after);
+      at.local = t - (__builtin_amdgcn_readlane(end, l) - __builtin_amdgcn_readlane(n, l));
+      at.q0 = __builtin_amdgcn_readlane(q0, l);
+      at.nq = __builtin_amdgcn_readlane(nq, l);
+      at.kv0 = __builtin_amdgcn_readlane(kv0, l);
+      at.nk = __builtin_amdgcn_readlane(nk, l);
+      return true;
+    }
+    t -= __builtin_amdgcn_readlane(end, 63);
+    if (t < 0) return false;      // offsets that overlap so often that the count wrapped
+  }
+  return false;
+}
+
+// v summed over lanes 0 .. this one.
+__device__ inline int sum_to_lane(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);     // 1, 2, 4, 8 lanes on in a row of 16
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);     // a row's last lane to the next row
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);     // lane 31 to the upper half
+  return v;
+}
+
+// find_tile with the sum over the lanes by DPP, none for a single sequence.
+__device__ inline bool find_tile_spans(const SpanParams& p, int rows, int t, int lane, Place& at) {
+  if (p.batch == 1) {
+    at.local = t;
+    span_uniform(p.cu_q, 0, p.total_q, at.q0, at.nq);
+    span_uniform(p.cu_k, 0, p.total_k, at.kv0, at.nk);
+    return t < (at.nq * p.group + rows - 1) / rows;
+  }
+  for (int base = 0; base < p.batch; base += 64) {
+    const int b = min(base + lane, p.batch - 1);
+    int q0, nq, kv0, nk;
+    span(p.cu_q, b, p.total_q, q0, nq);
+    span(p.cu_k, b, p.total_k, kv0, nk);
+    const int n = base + lane < p.batch ? (nq * p.group + rows - 1) / rows : 0;
+    const int end = sum_to_lane(n);
     const uint64_t after = __ballot(t < end);
     if (after) {
       const int l = __builtin_ctzll(after);
@@ -290,48 +340,24 @@ struct Work {
     wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     half = lane >> 5;
     col = lane & 31;
+    if constexpr (SPANS) return locate_spans();
     // blocks run over key heads first, then tiles, then shares (the first of
     // which every tile has)
-    bool pre = false;                                  // a workgroup of the cut-off prefix
-    int block = blockIdx.x, tiles = p.tiles;
-    if constexpr (SPANS)
-      if (p.pre_splits > 0) {
-        pre = block < p.pre_blocks();
-        if (pre)
-          tiles = p.pre_tiles;
-        else
-          block -= p.pre_blocks();
-      }
-    hk = block % p.heads_kv;
-    const int rest = block / p.heads_kv;
-    const int split = rest / tiles;
+    hk = blockIdx.x % p.heads_kv;
+    const int rest = blockIdx.x / p.heads_kv;
+    const int split = rest / p.tiles;
     Place at;
-    if (SPANS && pre) {
-      int last, more;
-      span(p.cu_q, 0, p.total_q, at.q0, at.nq);
-      span(p.cu_q, p.batch - 1, p.total_q, last, more);
-      at.nq = max(last + more - at.q0, 0);
-      at.local = rest % tiles;
-      at.kv0 = at.nk = 0;
-      if ((int64_t)at.local * T::ROWS >= (int64_t)at.nq * p.group) return false;
-    } else if (!find_tile(p, T::ROWS, rest % tiles, lane, at)) {
-      return false;
-    }
+    if (!find_tile(p, T::ROWS, rest % p.tiles, lane, at)) return false;
     int local = at.local;
     const int nq = at.nq;
     q0 = at.q0;
     kv0 = at.kv0;
     nk = at.nk;
-    shares = p.shares(p.keys(nk));
-    if constexpr (SPANS) {
-      if (pre) shares = p.pre_splits;
-      partial = shares > 1 || p.pre_splits > 0;
-      share = pre ? split : p.pre_splits + split;
-    }
+    shares = p.shares(nk);
     if (split >= shares) return false;
     const int nrows = nq * p.group;
     // causal tiles see more keys the later they are: start with the last
-    if (p.causal && !pre) local = (nrows + T::ROWS - 1) / T::ROWS - 1 - local;
+    if (p.causal) local = (nrows + T::ROWS - 1) / T::ROWS - 1 - local;
     row0 = local * T::ROWS;
     const int wrow0 = row0 + (MODE == kRows ? wave * kWaveRows : 0);
     row = wrow0 + col;
@@ -339,37 +365,91 @@ struct Work {
     const int rowc = min(row, nrows - 1);
     token = rowc / p.group;
     head = hk * p.group + (rowc - token * p.group);
-    int ntiles;
-    if constexpr (SPANS) {
-      auto look = [&](int r, int& l_, int& h_, int& f_) { p.view(min(r, nrows - 1) / p.group, nq, nk, l_, h_, f_); };
-      look(row, lo, hi, first);
-      int l0, h0, f0, l1, h1, f1;
-      look(wrow0, l0, h0, f0);
-      look(wrow0 + kWaveRows - 1, l1, h1, f1);
-      wlo = __builtin_amdgcn_readfirstlane(l1);
-      wfull = __builtin_amdgcn_readfirstlane(h0);
-      wfirst = __builtin_amdgcn_readfirstlane(f0);
-      wend = __builtin_amdgcn_readfirstlane(max(h1, f1));
-      look(row0, l0, h0, f0);
-      look(row0 + T::ROWS - 1, l1, h1, f1);
-      // the windows begin behind the first keys: every query of the tile sees all of those
-      const bool apart = l0 > f1;
-      na = __builtin_amdgcn_readfirstlane(pre || (p.prefix > 0 && p.pre_splits == 0) ? p.prefix : apart ? f1 : 0);
-      b0 = __builtin_amdgcn_readfirstlane(apart ? l0 : 0);
-      nb = __builtin_amdgcn_readfirstlane(max(max(h1, f1) - (apart ? l0 : 0), 0));
-      ta = (na + T::KT - 1) / T::KT;
-      ntiles = ta + (nb + T::KT - 1) / T::KT;
-      seen = na > 0 || hi > lo || first > 0;
-    } else {
-      const int shift = nk - nq;
-      auto visible = [&](int r) { return p.causal ? min(max(min(r, nrows - 1) / p.group + shift + 1, 0), nk) : nk; };
-      seen = visible(row);
-      wfull = __builtin_amdgcn_readfirstlane(visible(wrow0));
-      wend = __builtin_amdgcn_readfirstlane(visible(wrow0 + kWaveRows - 1));
-      ntiles = (visible(row0 + T::ROWS - 1) + T::KT - 1) / T::KT;
-    }
+    const int shift = nk - nq;
+    auto visible = [&](int r) { return p.causal ? min(max(min(r, nrows - 1) / p.group + shift + 1, 0), nk) : nk; };
+    seen = visible(row);
+    wfull = __builtin_amdgcn_readfirstlane(visible(wrow0));
+    wend = __builtin_amdgcn_readfirstlane(visible(wrow0 + kWaveRows - 1));
+    const int ntiles = (visible(row0 + T::ROWS - 1) + T::KT - 1) / T::KT;
     t0 = (int)((int64_t)ntiles * split / shares);
     t1 = (int)((int64_t)ntiles * (split + 1) / shares);
+    return true;
+  }
+
+  // The same for keys in two pieces.  A tile takes 10 to 20 us, so what stands before
+  // its first copy counts: no division is left but those of shares.
+  __device__ bool locate_spans() {
+    bool pre = false;                                  // a workgroup of the cut-off prefix
+    int block = blockIdx.x;
+    if (p.pre_splits > 0) {
+      pre = block < p.pre_blocks;
+      if (!pre) block -= p.pre_blocks;
+    }
+    const int rest = p.by_heads.of(block);
+    hk = block - rest * p.heads_kv;
+    const int split = (pre ? p.by_pre_tiles : p.by_tiles).of(rest);
+    Place at;
+    at.local = rest - split * (pre ? p.pre_tiles : p.tiles);
+    if (pre) {
+      int last, more;
+      span_uniform(p.cu_q, 0, p.total_q, at.q0, at.nq);
+      span_uniform(p.cu_q, p.batch - 1, p.total_q, last, more);
+      at.nq = max(last + more - at.q0, 0);
+      at.kv0 = at.nk = 0;
+      if (at.local >= (at.nq * p.group + T::ROWS - 1) / T::ROWS) return false;
+    } else if (!find_tile_spans(p, T::ROWS, at.local, lane, at)) {
+      return false;
+    }
+    q0 = at.q0;
+    kv0 = at.kv0;
+    nk = at.nk;
+    const int nq = at.nq;
+    shares = 1;
+    if (pre)
+      shares = p.pre_splits;
+    else if (p.splits > 1)
+      shares = p.shares(p.keys(nk));
+    partial = shares > 1 || p.pre_splits > 0;
+    share = pre ? split : p.pre_splits + split;
+    if (split >= shares) return false;
+    const int nrows = nq * p.group;
+    int local = at.local;
+    // causal tiles see more keys the later they are: start with the last
+    if (p.causal && !pre) local = (nrows + T::ROWS - 1) / T::ROWS - 1 - local;
+    row0 = local * T::ROWS;
+    const int wrow0 = row0 + (MODE == kRows ? wave * kWaveRows : 0);
+    row = wrow0 + col;
+    row_ok = row < nrows;
+    const int rowc = min(row, nrows - 1);
+    token = p.by_group.of(rowc);
+    head = hk * p.group + (rowc - token * p.group);
+    p.view(token, nq, nk, lo, hi, first);
+    int l0, h0, f0, l1, h1, f1;
+    p.view(p.by_group.of(min(wrow0, nrows - 1)), nq, nk, l0, h0, f0);
+    p.view(p.by_group.of(min(wrow0 + kWaveRows, nrows) - 1), nq, nk, l1, h1, f1);
+    wlo = l1;
+    wfull = h0;
+    wfirst = f0;
+    wend = max(h1, f1);
+    if constexpr (MODE == kRows) {
+      p.view(p.by_group.of(row0), nq, nk, l0, h0, f0);
+      p.view(p.by_group.of(min(row0 + T::ROWS, nrows) - 1), nq, nk, l1, h1, f1);
+    }
+    // the windows begin behind the first keys: every query of the tile sees all of those
+    const bool apart = l0 > f1;
+    na = pre || (p.prefix > 0 && p.pre_splits == 0) ? p.prefix : apart ? f1 : 0;
+    b0 = apart ? l0 : 0;
+    nb = max(max(h1, f1) - b0, 0);
+    ta = (na + T::KT - 1) / T::KT;
+    const int ntiles = ta + (nb + T::KT - 1) / T::KT;
+    seen = na > 0 || hi > lo || first > 0;
+    t0 = 0;
+    t1 = ntiles;
+    if (shares > 1) {                                  // ntiles split / shares, without 64 bits
+      const int q = ntiles / shares, r = ntiles - q * shares;
+      t0 = q * split + r * split / shares;
+      t1 = q * (split + 1) + r * (split + 1) / shares;
+    }
     return true;
   }
 
@@ -918,27 +998,12 @@ __global__ __launch_bounds__(NW * 64, H::DP == 64 ? 2 : 1) void attention_keys(c
 // share order in float32.  One wave per row: lane s holds share s's weight (at
 // most 64 shares), then each lane two channels, eight shares at a time.  A NaN
 // lse_s passes the maximum by and makes its weight, the sum and the row NaN.
+//
+// join_row: row `row` of tile number `tile` of the launch (row r of it), or with a cut-off prefix
+// the row by its query and head, whose shares lie at SpanParams::slot.
 template <bool SPANS>
-__global__ __launch_bounds__(256) void attention_join(const typename ParamsOf<SPANS>::type p, int rows_per_tile) {
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int hk = blockIdx.x % p.heads_kv;
-  const int rest = blockIdx.x / p.heads_kv;
-  const int tile = rest / (rows_per_tile / 4);
-  Place at;
-  if (!find_tile(p, rows_per_tile, tile, lane, at)) return;
-  const int shares = p.shares(p.keys(at.nk));
-  int pre = 0;                                           // shares of a prefix that was cut off
-  if constexpr (SPANS) pre = p.pre_splits;
-  if (shares + pre == 1) return;                         // written by its one share
-  const int nrows = at.nq * p.group;
-  int local = at.local;
-  if (p.causal) local = (nrows + rows_per_tile - 1) / rows_per_tile - 1 - local;
-  const int r = (rest % (rows_per_tile / 4)) * 4 + wave;          // row of the tile
-  const int row = local * rows_per_tile + r;
-  if (row >= nrows) return;
-  const int token = row / p.group;
-  const int head = hk * p.group + (row - token * p.group);
+__device__ inline void join_row(const typename ParamsOf<SPANS>::type& p, const Place& at, int shares, int pre, int tile,
+                                int rows_per_tile, int r, int token, int hk, int head, int lane) {
   auto slot = [&](int s) -> int64_t {
     if constexpr (SPANS)
       if (pre > 0) return p.slot(s, hk, at.q0 + token, head - hk * p.group);
@@ -969,7 +1034,7 @@ __global__ __launch_bounds__(256) void attention_join(const typename ParamsOf<SP
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       const float w = __shfl(weight, (s0 + u) & 63);
-      if (s0 + u < all && w != 0.f) {                 // a share without weight has written nothing
+      if (s0 + u < all && w != 0.f) {                    // a share without weight has written nothing
         a0 = __builtin_fmaf(w, v[u].x, a0);
         a1 = __builtin_fmaf(w, v[u].y, a1);
       }
@@ -988,6 +1053,51 @@ __global__ __launch_bounds__(256) void attention_join(const typename ParamsOf<SP
   if (p.lse && lane == 0)
     p.lse[(int64_t)head * p.total_q + at.q0 + token] =
         !none ? (top + __builtin_amdgcn_logf(sum)) * kLn2 : seen ? NAN : -INFINITY;
+}
+
+template <bool SPANS>
+__global__ __launch_bounds__(256) void attention_join(const typename ParamsOf<SPANS>::type p, int rows_per_tile) {
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int hk = blockIdx.x % p.heads_kv;
+  const int rest = blockIdx.x / p.heads_kv;
+  const int tile = rest / (rows_per_tile / 4);
+  Place at;
+  if (!find_tile(p, rows_per_tile, tile, lane, at)) return;
+  const int shares = p.shares(p.keys(at.nk));
+  if (shares == 1) return;                               // written by its one share
+  const int nrows = at.nq * p.group;
+  int local = at.local;
+  if (p.causal) local = (nrows + rows_per_tile - 1) / rows_per_tile - 1 - local;
+  const int r = (rest % (rows_per_tile / 4)) * 4 + wave;          // row of the tile
+  const int row = local * rows_per_tile + r;
+  if (row >= nrows) return;
+  const int token = row / p.group;
+  const int head = hk * p.group + (row - token * p.group);
+  join_row<SPANS>(p, at, shares, 0, tile, rows_per_tile, r, token, hk, head, lane);
+}
+
+// The join behind a cut-off prefix: a wave per query and head.
+__global__ __launch_bounds__(256) void attention_join_prefix(const SpanParams p) {
+  const int lane = threadIdx.x & 63;
+  const int id = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int query = id / p.heads_q, head = id - query * p.heads_q;
+  if (query >= p.total_q) return;
+  // the last sequence that begins at or before the query, 64 at a time
+  int b = -1;
+  for (int base = 0; base < p.batch; base += 64) {
+    const uint64_t m = __ballot(base + lane < p.batch && p.cu_q[min(base + lane, p.batch - 1)] <= query);
+    b += __builtin_popcountll(m);
+    if (m != ~uint64_t(0)) break;
+  }
+  if (b < 0) return;
+  Place at;
+  span(p.cu_q, b, p.total_q, at.q0, at.nq);
+  span(p.cu_k, b, p.total_k, at.kv0, at.nk);
+  const int token = query - at.q0;
+  if (token < 0 || token >= at.nq) return;
+  const int hk = p.by_group.of(head);
+  join_row<true>(p, at, p.shares(p.keys(at.nk)), p.pre_splits, 0, 0, 0, token, hk, head, lane);
 }
 
 // attention_keys' waves: so many that two workgroups fit a CU's LDS (a wave

@@ -69,6 +69,8 @@ SpanPlan plan_spans(const SpanArgs& a) {
   return sp;
 }
 
+int64_t join_blocks(int64_t total_q, int heads_q) { return (total_q * heads_q + 3) / 4; }
+
 template <class H>
 hipError_t launch(const SpanPlan& sp, const SpanParams& p, hipStream_t stream) {
   const Plan& pl = sp.own;
@@ -87,6 +89,11 @@ hipError_t launch(const SpanPlan& sp, const SpanParams& p, hipStream_t stream) {
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || sp.bytes == 0) return e;
+  if (sp.pre_splits > 0) {
+    const dim3 jgrid((unsigned)join_blocks(p.total_q, p.heads_q));
+    hipLaunchKernelGGL(attention_join_prefix, jgrid, dim3(256), 0, stream, p);
+    return hipGetLastError();
+  }
   const dim3 jgrid((unsigned)(pl.tiles * p.heads_kv * (pl.rows / 4)));
   hipLaunchKernelGGL((attention_join<true>), jgrid, dim3(256), 0, stream, p, pl.rows);
   return hipGetLastError();
@@ -98,6 +105,7 @@ size_t attention_spans_workspace(const SpanArgs& a) { return a.total_q == 0 ? 0 
 
 int64_t attention_spans_blocks(const SpanArgs& a) {
   const SpanPlan sp = plan_spans(a);
+  if (sp.pre_splits > 0) return std::max(sp.blocks, join_blocks(a.total_q, a.heads_q));
   return std::max(sp.blocks, sp.own.tiles * a.heads_kv * (sp.bytes > 0 ? sp.own.rows / 4 : 1));
 }
 
@@ -122,6 +130,11 @@ hipError_t launch_attention_spans(const SpanArgs& a, hipStream_t stream) {
   p.reach = (int)std::min(window_of(a) + sp.own.rows / p.group + 1, (double)INT32_MAX);
   p.pre_splits = sp.pre_splits;
   p.pre_tiles = sp.pre_tiles;
+  p.pre_blocks = sp.pre_splits * sp.pre_tiles * a.heads_kv;
+  p.by_heads = Quotient(a.heads_kv);
+  p.by_group = Quotient(p.group);
+  p.by_tiles = Quotient(p.tiles);
+  p.by_pre_tiles = Quotient(std::max(p.pre_tiles, 1));
   if (a.head_dim <= 64) return launch<Head<64, 4, 2>>(sp, p, stream);
   if (a.head_dim <= 96) return launch<Head<128, 6, 3>>(sp, p, stream);
   return launch<Head<128, 8, 4>>(sp, p, stream);

@@ -95,6 +95,19 @@ __device__ inline void lds_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
+// x / d for 0 <= x < 2^31 by a product: m = floor(2^(31 + s) / d) + 1 with 2^s >= d, whose
+// excess over the exact 2^(31 + s) / d is at most 2^s / d of a unit: x times it stays below one.
+struct Quotient {
+  uint32_t m;
+  int s;
+  explicit Quotient(int d = 1) {
+    s = 0;
+    while ((int64_t(1) << s) < d) ++s;
+    m = (uint32_t)((uint64_t(1) << (31 + s)) / d + 1);
+  }
+  __device__ int of(int x) const { return (int)(__umulhi(2u * (uint32_t)x, m) >> s); }
+};
+
 // Output activations of the GEMM epilogue (the values of svdq_activation).
 constexpr int kActNone = 0;
 constexpr int kActGeluTanh = 1;
