@@ -430,7 +430,8 @@ struct Work {
     wlo = l1;
     wfull = h0;
     wfirst = f0;
-    wend = max(h1, f1);
+    // a wave without rows works on nothing, one with rows on all of A
+    wend = MODE == kRows && wrow0 >= nrows ? INT32_MIN : max(max(h1, f1), 0);
     if constexpr (MODE == kRows) {
       p.view(p.by_group.of(row0), nq, nk, l0, h0, f0);
       p.view(p.by_group.of(min(row0 + T::ROWS, nrows) - 1), nq, nk, l1, h1, f1);
@@ -616,7 +617,7 @@ struct Work {
   }
   // Whether a query of the wave may see a key of tile t or of one after it.
   __device__ bool live(int t) const {
-    if constexpr (SPANS) return t < ta || b0 + (t - ta) * T::KT < wend;
+    if constexpr (SPANS) return b0 + (t - ta) * T::KT < wend;      // a tile of A lies in front of b0, or of 0
     return t * T::KT < wend;
   }
 
@@ -1203,7 +1204,10 @@ inline Plan plan_of(int total_q, int total_k, int batch, int heads_q, int heads_
     if (most > 1 && estimate(true, 4, std::max(mean, 2), longest) < estimate(true, 4, 1, longest)) pl.splits = (int)most;
   } else {
     offer(false, 4, 1, 0);
-    if (head_dim > 64 && !causal) offer(false, 8, 1, 0);    // causal: the finer grain balances the tiles' lengths
+    // causal: the finer grain balances the tiles' lengths; a window: the larger tile sees more keys
+    // that most of its rows do not, and nothing runs beside its start (16384 x 24 x 128, windows of
+    // 1025, 4097, 8193 keys: 453, 792, 1425 us with 4 waves, 489, 841, 1478 with 8)
+    if (head_dim > 64 && !causal && mean_own <= window) offer(false, 8, 1, 0);
     offer(true, 4, 1, 0);
     for (const int s : {2, 3, 4, 6, 8, 12, 16}) {
       const int chunk = (int)std::ceil(keys_of(kWaveRows) / s);

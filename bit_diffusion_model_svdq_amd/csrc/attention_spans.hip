@@ -22,6 +22,48 @@ double window_of(const SpanArgs& a) {
   return a.left < 0 || right < 0 ? INFINITY : (double)a.sinks + a.left + right + 1;
 }
 
+// Cuts the prefix off where that is less than the plan at hand: shares so long that the two
+// workgroups of a CU get one each on average.  attention_rows, whose four waves share a
+// tile of the prefix, where there are rows for them, and where the sequences' own tiles fill
+// the chip anyway; else attention_keys, more of whose waves work for each sequence.  Measured
+// (attention_keys / attention_rows / not cut off): prefix of 8192, 200 tokens x 32 / 8 x 128 135 / 72 /
+// 702 us, 64 45 / 35 / 181, 16 24 / 24 / 58; with 1000 keys of its own each 237 / 184 / 826, 77 / 78 / 221,
+// 31 / 40 / 64; 64 x 10 x 64 26 / 22 / 113, 16 17 / 18 / 42.  Prefix of 100, 16 tokens x 32 / 8 x 128
+// 12.7 / 12.6 / 10.5.
+void offer_cut(const SpanArgs& a, int64_t rows, SpanPlan& sp) {
+  const int64_t cus = device_cu_count();
+  const Cost cost = cost_of(a.head_dim);
+  const bool keys = rows < 4 * kWaveRows && std::min<int64_t>(a.batch, rows) * a.heads_kv < 2 * cus;
+  const int height = keys ? kWaveRows : 4 * kWaveRows;
+  const double turn = keys ? 32.0 * cost.keys_waves : 32.0, alone = keys ? cost.keys : cost.rows4;
+  const double each = keys ? cost.keys_each : cost.rows4_each;
+  const int64_t pre_tiles = (rows + height - 1) / height;
+  const int64_t tiles = std::min<int64_t>(rows / height + a.batch, rows);
+  const double mean_own = (double)a.total_k / a.batch;
+  // keys of all tiles; those of attention_rows against a sequence's own occupy one wave of four
+  const double pre_work = (double)pre_tiles * a.prefix * a.heads_kv, own_work = (double)tiles * mean_own * a.heads_kv;
+  const int64_t fair = (int64_t)std::min(std::ceil((pre_work + own_work) / (2.0 * cus) / 128) * 128, (double)INT32_MAX);
+  const int chunk = (int)std::max<int64_t>(256, fair);
+  const int pre_splits = (int)std::min<int64_t>((a.prefix + (int64_t)chunk - 1) / chunk, 32);
+  const int64_t want = std::max<int64_t>(4 * cus / std::max<int64_t>(tiles * a.heads_kv, 1), 1);
+  const int splits = (int)std::max<int64_t>(std::min<int64_t>({want, (a.total_k + (int64_t)chunk - 1) / chunk, 32}), 1);
+  const double longest = std::max((double)a.prefix / pre_splits, std::min(mean_own, (double)chunk));
+  const double us = std::max(std::ceil(longest / turn) * alone, (pre_work + (keys ? 1.0 : 0.6) * own_work) / turn / cus * each) + 3.0 +
+                    2e-6 * rows * a.heads_kv * (pre_splits + std::ceil(mean_own / chunk)) * a.head_dim;
+  const int64_t slots = rows * a.heads_kv * (pre_splits + splits);
+  if (us >= sp.own.us || slots * (a.head_dim + 1) * 4 > kMaxSplitBytes) return;
+  sp.own.us = us;
+  sp.pre_splits = pre_splits;
+  sp.pre_tiles = (int)pre_tiles;
+  sp.own.keys = keys;
+  sp.own.parts = keys ? 2 : 1;
+  sp.own.waves = 4;
+  sp.own.rows = height;
+  sp.own.splits = splits;
+  sp.own.chunk = chunk;
+  sp.own.tiles = tiles;
+}
+
 // A prefix is cut off where that is less work by the same estimate as in plan_of: new
 // tokens of several sequences, each of which would otherwise read it for itself, with most
 // of the MFMA's 32 columns idle.
@@ -31,34 +73,7 @@ SpanPlan plan_spans(const SpanArgs& a) {
   const int64_t rows = (int64_t)a.total_q * group;
   sp.own = plan_of(a.total_q, a.total_k, a.batch, a.heads_q, a.heads_kv, a.head_dim, a.causal != 0, window_of(a),
                    a.prefix);
-  if (a.prefix > 0 && a.batch > 1 && rows <= (int64_t)a.batch * kTokenRows) {
-    const int64_t cus = device_cu_count();
-    const Cost cost = cost_of(a.head_dim);
-    const int64_t pre_tiles = (rows + kWaveRows - 1) / kWaveRows;
-    const int64_t tiles = std::min<int64_t>(rows / kWaveRows + a.batch, rows);
-    const double mean_own = (double)a.total_k / a.batch;
-    const double keys = ((double)pre_tiles * a.prefix + (double)tiles * mean_own) * a.heads_kv;
-    const int64_t fair = (int64_t)std::min(std::ceil(keys / (2.0 * cus) / 128) * 128, (double)INT32_MAX);
-    const int chunk = (int)std::max<int64_t>(256, fair);
-    const int pre_splits = (int)std::min<int64_t>((a.prefix + (int64_t)chunk - 1) / chunk, 32);
-    const int64_t want = std::max<int64_t>(4 * cus / std::max<int64_t>(tiles * a.heads_kv, 1), 1);
-    const int splits = (int)std::max<int64_t>(std::min<int64_t>({want, (a.total_k + (int64_t)chunk - 1) / chunk, 32}), 1);
-    const double turn = 32.0 * cost.keys_waves;
-    const double longest = std::max((double)a.prefix / pre_splits, std::min(mean_own, (double)chunk));
-    const double us = std::max(std::ceil(longest / turn) * cost.keys, keys / turn / cus * cost.keys_each) + 4.0 +
-                      4.3e-6 * rows * a.heads_kv * (pre_splits + std::ceil(mean_own / chunk)) * a.head_dim;
-    const int64_t slots = rows * a.heads_kv * (pre_splits + splits);
-    if (us < sp.own.us && slots * (a.head_dim + 1) * 4 <= kMaxSplitBytes) {
-      sp.pre_splits = pre_splits;
-      sp.pre_tiles = (int)pre_tiles;
-      sp.own.keys = true;
-      sp.own.parts = 2;
-      sp.own.rows = kWaveRows;
-      sp.own.splits = splits;
-      sp.own.chunk = chunk;
-      sp.own.tiles = tiles;
-    }
-  }
+  if (a.prefix > 0 && a.batch > 1 && rows <= (int64_t)a.batch * kTokenRows) offer_cut(a, rows, sp);
   sp.blocks = (sp.own.tiles * sp.own.splits + (int64_t)sp.pre_tiles * sp.pre_splits) * a.heads_kv;
   if (sp.own.splits > 1 || sp.pre_splits > 0) {
     const size_t slots = sp.pre_splits > 0 ? (size_t)rows * a.heads_kv * (sp.pre_splits + sp.own.splits)
