@@ -87,10 +87,6 @@ struct Params {
   float* part_lse;       // [unit][rows], base 2; -inf: the share has no weight, and no row
 
   __device__ int shares(int nk) const { return min(nk > 0 ? (nk - 1) / chunk + 1 : 1, splits); }
-  __device__ int keys(int nk) const { return nk; }       // what the shares are cut from
-  __device__ bool sees(int token, int nq, int nk) const {
-    return (causal ? min(token + nk - nq + 1, nk) : nk) > 0;
-  }
 };
 
 // Keys in two pieces.  The tiles of piece A come first, all of whose keys every query
@@ -115,11 +111,11 @@ struct SpanParams : Params {
   int prefix;            // shared keys; 0 with a window or sinks
   int reach;             // own keys that a tile sees at most (sinks and window), for the shares
   int pre_splits, pre_tiles, pre_blocks;   // shares of the cut-off prefix, tiles of all rows; the launch's first workgroups
-  Quotient by_heads, by_group, by_tiles, by_pre_tiles;
+  Quotient by_heads, by_heads_q, by_group, by_tiles, by_pre_tiles;
 
   __device__ int keys(int nk) const { return min(nk, reach) + (pre_splits > 0 ? 0 : prefix); }
-  // With a cut-off prefix, the partial row of share s (its shares first) of a query's row:
-  // rows of sequences that fill little of their tiles take no more room for it.
+  // The partial row of share s (a cut-off prefix's first) of a query's row: sequences that
+  // fill little of their tiles take no more room for it.
   __device__ int64_t slot(int s, int hk, int query, int in_group) const {
     return ((int64_t)s * heads_kv + hk) * total_q * group + (int64_t)query * group + in_group;
   }
@@ -658,9 +654,11 @@ struct Work {
 #pragma unroll
         for (int j = 0; j < 16; ++j) o[i][j] = 0.f;
     if (part) {
-      int64_t slot = (int64_t)blockIdx.x * T::ROWS + (row - row0);
+      int64_t slot;
       if constexpr (SPANS)
-        if (p.pre_splits > 0) slot = p.slot(share, hk, q0 + token, head - hk * p.group);
+        slot = p.slot(share, hk, q0 + token, head - hk * p.group);
+      else
+        slot = (int64_t)blockIdx.x * T::ROWS + (row - row0);
       if (half == 0) p.part_lse[slot] = lse2;
       float* dst = p.part + slot * p.head_dim;
       if (!none) {
@@ -993,112 +991,6 @@ __global__ __launch_bounds__(NW * 64, H::DP == 64 ? 2 : 1) void attention_keys(c
   w.m = mn;
   w.l = sum;
   w.finish();
-}
-
-// Joins the shares of a tile's rows: weights 2^(lse_s - max), rows summed in
-// share order in float32.  One wave per row: lane s holds share s's weight (at
-// most 64 shares), then each lane two channels, eight shares at a time.  A NaN
-// lse_s passes the maximum by and makes its weight, the sum and the row NaN.
-//
-// join_row: row `row` of tile number `tile` of the launch (row r of it), or with a cut-off prefix
-// the row by its query and head, whose shares lie at SpanParams::slot.
-template <bool SPANS>
-__device__ inline void join_row(const typename ParamsOf<SPANS>::type& p, const Place& at, int shares, int pre, int tile,
-                                int rows_per_tile, int r, int token, int hk, int head, int lane) {
-  auto slot = [&](int s) -> int64_t {
-    if constexpr (SPANS)
-      if (pre > 0) return p.slot(s, hk, at.q0 + token, head - hk * p.group);
-    return (((int64_t)s * p.tiles + tile) * p.heads_kv + hk) * rows_per_tile + r;
-  };
-  const int all = shares + pre;
-  const int d = 2 * lane;
-  const bool on = d < p.head_dim;
-  // eight shares at a time; past the last one the last again, with weight 0
-  float2 v[8];
-  auto load = [&](int s0) {
-#pragma unroll
-    for (int u = 0; u < 8; ++u)
-      v[u] = *reinterpret_cast<const float2*>(p.part + slot(min(s0 + u, all - 1)) * p.head_dim + (on ? d : 0));
-  };
-  const float e = lane < all ? p.part_lse[slot(lane)] : -INFINITY;
-  load(0);                                               // beside the weights' loads
-  float top = e;
-#pragma unroll
-  for (int s = 32; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor(top, s));
-  const float weight = e == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(e - top);
-  float sum = weight;
-#pragma unroll
-  for (int s = 32; s > 0; s >>= 1) sum += __shfl_xor(sum, s);
-  float a0 = 0.f, a1 = 0.f;
-  for (int s0 = 0; s0 < all; s0 += 8) {
-    if (s0 > 0) load(s0);
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const float w = __shfl(weight, (s0 + u) & 63);
-      if (s0 + u < all && w != 0.f) {                    // a share without weight has written nothing
-        a0 = __builtin_fmaf(w, v[u].x, a0);
-        a1 = __builtin_fmaf(w, v[u].y, a1);
-      }
-    }
-  }
-  // as in finish(): no weight at all is NaN for a query that sees keys
-  const bool seen = p.sees(token, at.nq, at.nk);
-  const bool none = sum == 0.f;
-  const float inv = !none ? 1.f / sum : seen ? NAN : 0.f;
-  if (on) {
-    const uint16_t x = __builtin_bit_cast(uint16_t, (__bf16)(a0 * inv));
-    const uint16_t y = __builtin_bit_cast(uint16_t, (__bf16)(a1 * inv));
-    *reinterpret_cast<uint32_t*>(p.O + (int64_t)(at.q0 + token) * p.ldo + (int64_t)head * p.head_dim + d) =
-        x | ((uint32_t)y << 16);
-  }
-  if (p.lse && lane == 0)
-    p.lse[(int64_t)head * p.total_q + at.q0 + token] =
-        !none ? (top + __builtin_amdgcn_logf(sum)) * kLn2 : seen ? NAN : -INFINITY;
-}
-
-template <bool SPANS>
-__global__ __launch_bounds__(256) void attention_join(const typename ParamsOf<SPANS>::type p, int rows_per_tile) {
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int hk = blockIdx.x % p.heads_kv;
-  const int rest = blockIdx.x / p.heads_kv;
-  const int tile = rest / (rows_per_tile / 4);
-  Place at;
-  if (!find_tile(p, rows_per_tile, tile, lane, at)) return;
-  const int shares = p.shares(p.keys(at.nk));
-  if (shares == 1) return;                               // written by its one share
-  const int nrows = at.nq * p.group;
-  int local = at.local;
-  if (p.causal) local = (nrows + rows_per_tile - 1) / rows_per_tile - 1 - local;
-  const int r = (rest % (rows_per_tile / 4)) * 4 + wave;          // row of the tile
-  const int row = local * rows_per_tile + r;
-  if (row >= nrows) return;
-  const int token = row / p.group;
-  const int head = hk * p.group + (row - token * p.group);
-  join_row<SPANS>(p, at, shares, 0, tile, rows_per_tile, r, token, hk, head, lane);
-}
-
-// The join behind a cut-off prefix: a wave per query and head.
-__global__ __launch_bounds__(256) void attention_join_prefix(const SpanParams p) {
-  const int lane = threadIdx.x & 63;
-  const int id = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int query = id / p.heads_q, head = id - query * p.heads_q;
-  if (query >= p.total_q) return;
-  // the last sequence that begins at or before the query, 64 at a time
-  int b = -1;
-  for (int base = 0; base < p.batch; base += 64) {
-    const uint64_t m = __ballot(base + lane < p.batch && p.cu_q[min(base + lane, p.batch - 1)] <= query);
-    b += __builtin_popcountll(m);
-    if (m != ~uint64_t(0)) break;
-  }
-  if (b < 0) return;
-  Place at;
-  span(p.cu_q, b, p.total_q, at.q0, at.nq);
-  span(p.cu_k, b, p.total_k, at.kv0, at.nk);
-  const int token = query - at.q0;
-  if (token < 0 || token >= at.nq) return;
-  const int hk = p.by_group.of(head);
-  join_row<true>(p, at, p.shares(p.keys(at.nk)), p.pre_splits, 0, 0, 0, token, hk, head, lane);
 }
 
 // attention_keys' waves: so many that two workgroups fit a CU's LDS (a wave
