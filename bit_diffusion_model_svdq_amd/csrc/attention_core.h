@@ -1002,15 +1002,7 @@ constexpr int key_waves(int dp) { return dp == 64 ? 4 : 2; }
 // Rows per sequence, on average, up to which a call counts as one of new tokens.
 constexpr int kTokenRows = 64;
 
-struct Plan {
-  bool keys = false;      // attention_keys: 32 rows per workgroup
-  int parts = 1;          // of a weight in P V
-  int waves = 4;          // of a workgroup
-  int rows = 0, splits = 1, chunk = 0;
-  int64_t tiles = 0;      // at most, over the packed batch
-  double us = 0;          // the estimate
-  size_t part = 0, bytes = 0;
-};
+using Plan = AttentionPlan;
 
 // What a tile of 32 keys costs a workgroup, in us, by the head's size (up to 64,
 // 96, 128 channels): alone on its CU, where latency counts, and as its part of a

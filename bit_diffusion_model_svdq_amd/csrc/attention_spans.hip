@@ -84,12 +84,8 @@ __global__ __launch_bounds__(256) void attention_join_spans(const SpanParams p) 
 // Partial rows of a cut-off prefix that a call may ask its caller to hold: 8192 new tokens x 32 x 128.
 constexpr int64_t kMaxSplitBytes = int64_t(256) << 20;
 
-struct SpanPlan {
-  Plan own;               // the whole work, or with a cut-off prefix that against the own keys
-  int pre_splits = 0, pre_tiles = 0;
-  int64_t blocks = 0;     // workgroups of the launch
-  size_t part = 0, bytes = 0;
-};
+// Workgroups of the join.
+int64_t join_blocks(int64_t total_q, int heads_q) { return (total_q * heads_q + 3) / 4; }
 
 // Own keys that a query sees at most.
 double window_of(const SpanArgs& a) {
@@ -150,15 +146,15 @@ SpanPlan plan_spans(const SpanArgs& a) {
                    a.prefix);
   if (a.prefix > 0 && a.batch > 1 && rows <= (int64_t)a.batch * kTokenRows) offer_cut(a, rows, sp);
   sp.blocks = (sp.own.tiles * sp.own.splits + (int64_t)sp.pre_tiles * sp.pre_splits) * a.heads_kv;
+  sp.most_blocks = sp.blocks;
   if (sp.own.splits > 1 || sp.pre_splits > 0) {
     const size_t slots = (size_t)rows * a.heads_kv * (sp.pre_splits + sp.own.splits);
     sp.part = (slots * a.head_dim * 4 + 255) & ~size_t(255);
     sp.bytes = sp.part + ((slots * 4 + 255) & ~size_t(255));
+    sp.most_blocks = std::max(sp.blocks, join_blocks(a.total_q, a.heads_q));
   }
   return sp;
 }
-
-int64_t join_blocks(int64_t total_q, int heads_q) { return (total_q * heads_q + 3) / 4; }
 
 template <class H>
 hipError_t launch(const SpanPlan& sp, const SpanParams& p, hipStream_t stream) {
@@ -184,15 +180,9 @@ hipError_t launch(const SpanPlan& sp, const SpanParams& p, hipStream_t stream) {
 
 }  // namespace
 
-size_t attention_spans_workspace(const SpanArgs& a) { return a.total_q == 0 ? 0 : plan_spans(a).bytes; }
+SpanPlan plan_attention_spans(const SpanArgs& a) { return plan_spans(a); }
 
-int64_t attention_spans_blocks(const SpanArgs& a) {
-  const SpanPlan sp = plan_spans(a);
-  return sp.bytes > 0 ? std::max(sp.blocks, join_blocks(a.total_q, a.heads_q)) : sp.blocks;
-}
-
-hipError_t launch_attention_spans(const SpanArgs& a, hipStream_t stream) {
-  const SpanPlan sp = plan_spans(a);
+hipError_t launch_attention_spans(const SpanArgs& a, const SpanPlan& sp, hipStream_t stream) {
   SpanParams p;
   p.Q = a.Q; p.K = a.K; p.V = a.V; p.O = a.O; p.lse = a.lse;
   p.ldq = a.ldq; p.ldk = a.ldk; p.ldv = a.ldv; p.ldo = a.ldo;

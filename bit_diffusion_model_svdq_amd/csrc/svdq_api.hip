@@ -272,7 +272,7 @@ constexpr int64_t kMaxBlocks = (int64_t(1) << 23) - 1;
 constexpr int kMaxHeads = 1 << 20;
 
 svdq_status check_attention_shape(int batch, int64_t total_q, int64_t total_k, int heads_q, int heads_kv,
-                                  int head_dim) {
+                                  int head_dim, bool count_blocks = true) {
   if (batch < 1) return fail(SVDQ_ERR_INVALID_ARG, "batch must be >= 1 (got %d)", batch);
   if (total_q < 0 || total_k < 0)
     return fail(SVDQ_ERR_INVALID_ARG, "negative total_q=%lld or total_k=%lld", (long long)total_q,
@@ -287,7 +287,7 @@ svdq_status check_attention_shape(int batch, int64_t total_q, int64_t total_k, i
   if (total_q > INT32_MAX || total_k > INT32_MAX - 512 || total_q * (heads_q / heads_kv) > INT32_MAX - 512)
     return fail(SVDQ_ERR_INVALID_ARG, "total_q=%lld (times %d heads a group) or total_k=%lld is beyond 31 bits less 512",
                 (long long)total_q, heads_q / heads_kv, (long long)total_k);
-  if (total_q > 0 && attention_blocks((int)total_q, (int)total_k, batch, heads_q, heads_kv, head_dim) > kMaxBlocks)
+  if (count_blocks && total_q > 0 && attention_blocks((int)total_q, (int)total_k, batch, heads_q, heads_kv, head_dim) > kMaxBlocks)
     return fail(SVDQ_ERR_INVALID_ARG, "too many rows for one launch: total_q=%lld, heads_q=%d, batch=%d",
                 (long long)total_q, heads_q, batch);
   return SVDQ_OK;
@@ -335,18 +335,20 @@ svdq_status check_workspace(const void* workspace, size_t bytes, size_t need) {
   return SVDQ_OK;
 }
 
-// The shape of an attention call whose keys lie in two pieces.
-svdq_status check_spans_shape(const SpanArgs& a, int64_t total_q, int64_t total_k, int64_t prefix) {
+// The shape of an attention call whose keys lie in two pieces, and its plan.
+svdq_status check_spans_shape(const SpanArgs& a, int64_t total_q, int64_t total_k, int64_t prefix, SpanPlan& plan) {
   if (prefix < 0 || prefix > INT32_MAX - 512)
     return fail(SVDQ_ERR_INVALID_ARG, "the prefix' %lld keys are negative or beyond 31 bits less 512", (long long)prefix);
-  SVDQ_TRY(check_attention_shape(a.batch, total_q, total_k, a.heads_q, a.heads_kv, a.head_dim));
+  SVDQ_TRY(check_attention_shape(a.batch, total_q, total_k, a.heads_q, a.heads_kv, a.head_dim, false));
   if (total_k + prefix > INT32_MAX - 512)
     return fail(SVDQ_ERR_INVALID_ARG, "total_k=%lld and the prefix' %lld keys are beyond 31 bits less 512",
                 (long long)total_k, (long long)prefix);
   if (a.left < -1 || a.right < -1)
     return fail(SVDQ_ERR_INVALID_ARG, "window_left=%d and window_right=%d must be -1 or more", a.left, a.right);
   if (a.sinks < 0) return fail(SVDQ_ERR_INVALID_ARG, "sinks must not be negative (got %d)", a.sinks);
-  if (total_q > 0 && attention_spans_blocks(a) > kMaxBlocks)
+  if (total_q == 0) return SVDQ_OK;
+  plan = plan_attention_spans(a);
+  if (plan.most_blocks > kMaxBlocks)
     return fail(SVDQ_ERR_INVALID_ARG, "too many rows for one launch: total_q=%lld, heads_q=%d, batch=%d",
                 (long long)total_q, a.heads_q, a.batch);
   return SVDQ_OK;
@@ -611,7 +613,8 @@ size_t svdq_attention_window_workspace_bytes(int64_t total_q, int64_t total_k, i
                                              int head_dim, int causal, int window_left, int window_right, int sinks) {
   const SpanArgs a = spans_of(batch, total_q, total_k, heads_q, heads_kv, head_dim, causal, window_left, window_right,
                               sinks, 0);
-  return check_spans_shape(a, total_q, total_k, 0) == SVDQ_OK ? attention_spans_workspace(a) : 0;
+  SpanPlan plan;
+  return check_spans_shape(a, total_q, total_k, 0, plan) == SVDQ_OK ? plan.bytes : 0;
 }
 
 svdq_status svdq_attention_window_forward(const uint16_t* Q, int64_t ldq, const uint16_t* K, int64_t ldk,
@@ -623,20 +626,22 @@ svdq_status svdq_attention_window_forward(const uint16_t* Q, int64_t ldq, const 
   return guarded([&]() -> svdq_status {
     SpanArgs a = spans_of(batch, total_q, total_k, heads_q, heads_kv, head_dim, causal, window_left, window_right,
                           sinks, 0);
-    SVDQ_TRY(check_spans_shape(a, total_q, total_k, 0));
+    SpanPlan plan;
+    SVDQ_TRY(check_spans_shape(a, total_q, total_k, 0, plan));
     static_cast<AttentionArgs&>(a) = {Q, K, V, ldq, ldk, ldv, ldo, cu_q, cu_k, batch, a.total_q, a.total_k, heads_q,
                                       heads_kv, head_dim, scale, causal, O, lse, workspace};
     SVDQ_TRY(check_attention_call(a));
     if (total_q == 0) return SVDQ_OK;
-    SVDQ_TRY(check_workspace(workspace, workspace_bytes, attention_spans_workspace(a)));
-    return hip_check(launch_attention_spans(a, static_cast<hipStream_t>(stream)), "attention_window launch");
+    SVDQ_TRY(check_workspace(workspace, workspace_bytes, plan.bytes));
+    return hip_check(launch_attention_spans(a, plan, static_cast<hipStream_t>(stream)), "attention_window launch");
   });
 }
 
 size_t svdq_attention_prefix_workspace_bytes(int64_t total_q, int64_t prefix_len, int64_t total_k, int batch,
                                              int heads_q, int heads_kv, int head_dim, int causal) {
   const SpanArgs a = spans_of(batch, total_q, total_k, heads_q, heads_kv, head_dim, causal, -1, -1, 0, prefix_len);
-  return check_spans_shape(a, total_q, total_k, prefix_len) == SVDQ_OK ? attention_spans_workspace(a) : 0;
+  SpanPlan plan;
+  return check_spans_shape(a, total_q, total_k, prefix_len, plan) == SVDQ_OK ? plan.bytes : 0;
 }
 
 svdq_status svdq_attention_prefix_forward(const uint16_t* Q, int64_t ldq, const uint16_t* prefix_K, int64_t ldpk,
@@ -648,7 +653,8 @@ svdq_status svdq_attention_prefix_forward(const uint16_t* Q, int64_t ldq, const 
                                           size_t workspace_bytes, void* stream) {
   return guarded([&]() -> svdq_status {
     SpanArgs a = spans_of(batch, total_q, total_k, heads_q, heads_kv, head_dim, causal, -1, -1, 0, prefix_len);
-    SVDQ_TRY(check_spans_shape(a, total_q, total_k, prefix_len));
+    SpanPlan plan;
+    SVDQ_TRY(check_spans_shape(a, total_q, total_k, prefix_len, plan));
     static_cast<AttentionArgs&>(a) = {Q, K, V, ldq, ldk, ldv, ldo, cu_q, cu_k, batch, a.total_q, a.total_k, heads_q,
                                       heads_kv, head_dim, scale, causal, O, lse, workspace};
     SVDQ_TRY(check_attention_call(a));
@@ -664,8 +670,8 @@ svdq_status svdq_attention_prefix_forward(const uint16_t* Q, int64_t ldq, const 
     a.PV = prefix_V;
     a.ldpk = ldpk;
     a.ldpv = ldpv;
-    SVDQ_TRY(check_workspace(workspace, workspace_bytes, attention_spans_workspace(a)));
-    return hip_check(launch_attention_spans(a, static_cast<hipStream_t>(stream)), "attention_prefix launch");
+    SVDQ_TRY(check_workspace(workspace, workspace_bytes, plan.bytes));
+    return hip_check(launch_attention_spans(a, plan, static_cast<hipStream_t>(stream)), "attention_prefix launch");
   });
 }
 

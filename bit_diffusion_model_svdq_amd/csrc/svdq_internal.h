@@ -161,6 +161,17 @@ hipError_t launch_fused_smallk_mx(const FusedPlan& plan, const uint16_t* X, int 
                                   uint16_t* Y, int act, uint8_t* dbg_qx, uint8_t* dbg_sx,
                                   hipStream_t stream);
 
+// How an attention call is launched (attention_core.h).
+struct AttentionPlan {
+  bool keys = false;      // attention_keys: 32 rows per workgroup
+  int parts = 1;          // of a weight in P V
+  int waves = 4;          // of a workgroup
+  int rows = 0, splits = 1, chunk = 0;
+  int64_t tiles = 0;      // at most, over the packed batch
+  double us = 0;          // the estimate
+  size_t part = 0, bytes = 0;
+};
+
 // Attention over packed sequences (svdq_attention_forward).  cu_q / cu_k: row
 // offsets on the device, or NULL for one sequence of all rows.  workspace: the
 // bytes attention_workspace() gives (0: none needed).
@@ -191,9 +202,15 @@ struct SpanArgs : AttentionArgs {
   int64_t ldpk, ldpv;
   int prefix;
 };
-size_t attention_spans_workspace(const SpanArgs& a);     // from the sizes, causal and the window alone
-int64_t attention_spans_blocks(const SpanArgs& a);
-hipError_t launch_attention_spans(const SpanArgs& a, hipStream_t stream);
+struct SpanPlan {
+  AttentionPlan own;      // the whole work, or with a cut-off prefix that against the own keys
+  int pre_splits = 0, pre_tiles = 0;
+  int64_t blocks = 0;     // workgroups of the launch
+  int64_t most_blocks = 0;     // and of the largest of its launches
+  size_t part = 0, bytes = 0;  // of the workspace
+};
+SpanPlan plan_attention_spans(const SpanArgs& a);     // from the sizes, causal and the window alone
+hipError_t launch_attention_spans(const SpanArgs& a, const SpanPlan& plan, hipStream_t stream);
 
 // Norms (the values of svdq_norm) and svdq_block_norm_forward's operands; NULL
 // where absent, row strides of the per-sequence vectors in elements.
