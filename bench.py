@@ -28,8 +28,8 @@ MLP up 3072 -> 12288 with GELU fused into its epilogue, MLP down
 seeded rank-16 LoRA to r = 48; the attention itself is not part of it.
 --workload dit_block_full times the whole block: the modulation linear (bf16), norm and
 modulation, those four linears, attention with 24 heads of 128 channels over the fused QKV
-output, and the two calls of gate, residual (and norm) between them; a model's norm of the
-queries and keys and its rotary step are not part of it.
+output, and the two calls of gate, residual (and norm) between them; with --rope also the
+norm of the queries and keys and their rotation, in place on the QKV output.
 """
 from __future__ import annotations
 
@@ -74,6 +74,8 @@ def parse():
     ap.add_argument("--path", choices=["auto", "two-kernel"], default="auto",
                     help="auto: the forward's own plan (one fused kernel for narrow layers); "
                          "two-kernel: the quantize kernel then the GEMM, always")
+    ap.add_argument("--rope", action="store_true",
+                    help="dit_block_full: with the norm of queries and keys and their rotation before attention")
     ap.add_argument("--no-graph", action="store_true",
                     help="report the eager launch loop instead of the HIP graph replay")
     return ap.parse_args()
@@ -679,7 +681,19 @@ def bench_block_full(args, S, synth, torch):
                                   S.SVDQ_NORM_NONE if h is None else S.SVDQ_NORM_LAYER, None, None, scale, shift,
                                   1e-6, x_out, h)
 
-    STEPS = ("modulation", "norm", "qkv", "attention", "out", "gate_norm", "up", "down", "gate")
+    STEPS = ("modulation", "norm", "qkv") + (("rope",) if args.rope else ()) + (
+        "attention", "out", "gate_norm", "up", "down", "gate")
+    if args.rope:
+        wq, wk = 1 + normal(D, std=0.1), 1 + normal(D, std=0.1)
+        angle = (torch.arange(M, dtype=torch.float64, device=dev)[:, None]
+                 * 10000.0 ** (-torch.arange(0, D, 2, dtype=torch.float64, device=dev) / D))
+        cos, sin = angle.cos().float(), angle.sin().float()
+
+    def rope(d):
+        v = d["qkv"]["Y"].view(bf16).view(M, 3 * heads, D)
+        q, k = v[:, :heads], v[:, heads:2 * heads]
+        S.svdq_qk_norm_rope_forward(q, k, None, None, S.SVDQ_NORM_RMS, wq, None, wk, None, 1e-6, cos, sin,
+                                    S.SVDQ_ROPE_NEIGHBOURS, q, k)
 
     def run(d, ev=None):
         sh1, sc1, g1, sh2, sc2, g2 = d["mod"].split(C, dim=1)
@@ -687,6 +701,7 @@ def bench_block_full(args, S, synth, torch):
             lambda: S.svdq_linear_bf16_forward(d["e"], d["Wm"], d["bm"], S.SVDQ_ACT_NONE, None, d["mod"], d["work"]),
             lambda: norm(d, d["x"], None, None, sc1, sh1, None, d["h"]),
             lambda: svdq(d, "qkv", d["h"]),
+            *([lambda: rope(d)] if args.rope else []),
             lambda: attention(d),
             lambda: svdq(d, "out", d["a"].view(M, C)),
             lambda: norm(d, d["x"], d["out"]["Y"].view(bf16), g1, sc2, sh2, d["x1"], d["h"]),
@@ -718,7 +733,7 @@ def bench_block_full(args, S, synth, torch):
     dur = np.array([[e[j].elapsed_time(e[j + 1]) for j in range(len(STEPS))] for e in evs]).mean(axis=0)
     if not args.no_graph:
         ms_step = time_graph(torch, lambda i: run(sets[i % nsets]), args.steps)
-    att_us = round(float(dur[3]) * 1e3, 3)
+    att_us = round(float(dur[STEPS.index("attention")]) * 1e3, 3)
     if not args.no_graph:
         att_us = round(time_graph(torch, lambda i: attention(sets[i % nsets]), args.steps) * 1e3, 3)
     att_ops = 4.0 * M * M * C
@@ -738,7 +753,8 @@ def bench_block_full(args, S, synth, torch):
         "dtype": f"{'mxfp4' if mx else 'int4'} linears, bf16 attention, norms and modulation",
         "data": "synthetic",
         "config": {"workload": "dit_block_full", "format": args.format, "M": M, "width": C, "heads": heads,
-                   "rank": layers[0]["r"], "rotated_sets": nsets, "hip_graph": not args.no_graph},
+                   "rank": layers[0]["r"], "rotated_sets": nsets, "hip_graph": not args.no_graph,
+                   **({"rope": True} if args.rope else {})},
         "eager_ms_per_step": round(eager_ms_step, 5),
         "tokens_per_s": round(M / (ms_step * 1e-3), 1),
         "roofline": {"kernel": "attention", "bound": "mfma", "achieved": round(achieved, 2), "peak": PEAK_BF16_TFLOPS,
