@@ -515,10 +515,10 @@ struct Work {
     int64_t key;
     if (c.own) {
       key = (int64_t)kv0 + b0 + (int64_t)(t - ta) * T::KT;
-      c.left = nb - (t - ta) * T::KT;
+      c.left = min(nb, (t1 - ta) * T::KT) - (t - ta) * T::KT;      // a share copies no tile of the next one
     } else {
       key = (int64_t)t * T::KT;
-      c.left = na - t * T::KT;
+      c.left = min(na, t1 * T::KT) - t * T::KT;
       if (p.prefix > 0) {
         base = K ? p.PK : p.PV;
         ld = K ? p.ldpk : p.ldpv;
@@ -591,7 +591,7 @@ struct Work {
   __device__ void mask(f32x16& s, int t) const {
     if constexpr (SPANS) {
       const int at = b0 + (t - ta) * T::KT;
-      uint32_t bits = t < ta ? below(na - t * T::KT) : (below(hi - at) & ~below(lo - at)) | below(first - at);
+      uint32_t bits = t >= t1 ? 0u : t < ta ? below(na - t * T::KT) : (below(hi - at) & ~below(lo - at)) | below(first - at);
       bits >>= 4 * half;
 #pragma unroll
       for (int j = 0; j < 16; ++j)
@@ -607,6 +607,7 @@ struct Work {
   __device__ bool whole(int t) const {
     if constexpr (SPANS) {
       const int at = b0 + (t - ta) * T::KT, end = at + T::KT;
+      if (t >= t1) return false;
       return t < ta ? (t + 1) * T::KT <= na : (at >= wlo && end <= wfull) || end <= wfirst;
     }
     return t * T::KT + T::KT <= wfull;
