@@ -430,11 +430,11 @@ svdq_status svdq_attention_forward(const uint16_t* Q, int64_t ldq, const uint16_
  *   (p - window_left <= j <= p + window_right  or  j < sinks)  and  (not causal  or  j <= p).
  * window_left, window_right: -1 for no limit on that side, else 0 or more; sinks: 0 or
  * more (more than there are keys: all).  Everything else is svdq_attention_forward's, with
- * this about non-finite K and V: what lies in front of all the windows of 32 (calls with
- * few rows) to 256 rows that are worked on together and behind the sinks, or behind all of
- * their keys, is not read (keys that a rolling cache has given up may hold
- * anything).  Keys between, which some of those queries see and others do not, can reach
- * all of them. */
+ * this about non-finite K and V: rows (queries times heads of a group) are worked on 32, 128
+ * or 256 together, and of the keys behind the sinks those in front of all their windows, and
+ * those behind all that they see, are not read: what a rolling cache has given up may hold
+ * anything.  Keys between, which some of these queries see and others do not, can reach all
+ * of them. */
 size_t svdq_attention_window_workspace_bytes(int64_t total_q, int64_t total_k, int batch, int heads_q,
                                              int heads_kv, int head_dim, int causal, int window_left,
                                              int window_right, int sinks);
@@ -449,10 +449,13 @@ svdq_status svdq_attention_window_forward(const uint16_t* Q, int64_t ldq, const 
 /* svdq_attention_forward for sequences that begin alike: every query sees the prefix_len
  * keys of prefix_K, prefix_V [prefix_len, heads_kv, head_dim] (rows ldpk, ldpv elements
  * apart, as ldk and ldv), then the keys of its own sequence (causal: those up to its
- * own, as there).  One softmax over both; the prefix is stored once, and calls of few rows
- * per sequence also read and compute it once for all of them.  Everything else is
- * svdq_attention_forward's; either of the two pieces may be empty, also for some
- * of the sequences.  prefix_len + total_k: at most 2^31 - 513. */
+ * own, as there).  One softmax over both; the prefix is stored once, and calls of at most 64
+ * rows per sequence also read and compute it once for all sequences where that is less work.
+ * Then the softmax's weights enter the product with V rounded to bf16 where there are many
+ * rows, with 15 bits where there are few.  Everything else is svdq_attention_forward's; either
+ * of the two pieces may be empty, also for some of the sequences.  prefix_len + total_k: at
+ * most 2^31 - 513.  The workspace of new tokens grows with them (partial rows of float32), to
+ * at most 257 MiB. */
 size_t svdq_attention_prefix_workspace_bytes(int64_t total_q, int64_t prefix_len, int64_t total_k, int batch,
                                              int heads_q, int heads_kv, int head_dim, int causal);
 svdq_status svdq_attention_prefix_forward(const uint16_t* Q, int64_t ldq, const uint16_t* prefix_K,
