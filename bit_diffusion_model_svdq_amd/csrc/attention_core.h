@@ -202,13 +202,6 @@ __device__ inline void span(const int32_t* cu, int b, int total, int& begin, int
   len = max(min(hi, total) - begin, 0);
 }
 
-// span() of one sequence, known to be the same in all lanes.
-__device__ inline void span_uniform(const int32_t* cu, int b, int total, int& begin, int& len) {
-  span(cu, b, total, begin, len);
-  begin = __builtin_amdgcn_readfirstlane(begin);
-  len = __builtin_amdgcn_readfirstlane(len);
-}
-
 // Where a tile lies: its number in its sequence, and the sequence's rows.
 struct Place {
   int local, q0, nq, kv0, nk;
@@ -258,19 +251,36 @@ __device__ inline int sum_to_lane(int v) {
   return v;
 }
 
+// Sequence b's rows of both kinds.  The four offsets are loaded together: one after the
+// other, behind each test for NULL, they cost a memory latency each.
+__device__ inline void spans_of(const SpanParams& p, int b, int& q0, int& nq, int& kv0, int& nk) {
+  if (p.cu_q && p.cu_k) {
+    const int qa = p.cu_q[b], qb = p.cu_q[b + 1], ka = p.cu_k[b], kb = p.cu_k[b + 1];
+    q0 = min(max(qa, 0), p.total_q);
+    nq = max(min(qb, p.total_q) - q0, 0);
+    kv0 = min(max(ka, 0), p.total_k);
+    nk = max(min(kb, p.total_k) - kv0, 0);
+  } else {
+    span(p.cu_q, b, p.total_q, q0, nq);
+    span(p.cu_k, b, p.total_k, kv0, nk);
+  }
+}
+
 // find_tile with the sum over the lanes by DPP, none for a single sequence.
 __device__ inline bool find_tile_spans(const SpanParams& p, int rows, int t, int lane, Place& at) {
   if (p.batch == 1) {
+    spans_of(p, 0, at.q0, at.nq, at.kv0, at.nk);
     at.local = t;
-    span_uniform(p.cu_q, 0, p.total_q, at.q0, at.nq);
-    span_uniform(p.cu_k, 0, p.total_k, at.kv0, at.nk);
+    at.q0 = __builtin_amdgcn_readfirstlane(at.q0);
+    at.nq = __builtin_amdgcn_readfirstlane(at.nq);
+    at.kv0 = __builtin_amdgcn_readfirstlane(at.kv0);
+    at.nk = __builtin_amdgcn_readfirstlane(at.nk);
     return t < (at.nq * p.group + rows - 1) / rows;
   }
   for (int base = 0; base < p.batch; base += 64) {
     const int b = min(base + lane, p.batch - 1);
     int q0, nq, kv0, nk;
-    span(p.cu_q, b, p.total_q, q0, nq);
-    span(p.cu_k, b, p.total_k, kv0, nk);
+    spans_of(p, b, q0, nq, kv0, nk);
     const int n = base + lane < p.batch ? (nq * p.group + rows - 1) / rows : 0;
     const int end = sum_to_lane(n);
     const uint64_t after = __ballot(t < end);
@@ -387,10 +397,9 @@ struct Work {
     Place at;
     at.local = rest - split * (pre ? p.pre_tiles : p.tiles);
     if (pre) {
-      int last, more;
-      span_uniform(p.cu_q, 0, p.total_q, at.q0, at.nq);
-      span_uniform(p.cu_q, p.batch - 1, p.total_q, last, more);
-      at.nq = max(last + more - at.q0, 0);
+      const int begin = p.cu_q[0], end = p.cu_q[p.batch];      // batch > 1: not NULL
+      at.q0 = __builtin_amdgcn_readfirstlane(min(max(begin, 0), p.total_q));
+      at.nq = max(__builtin_amdgcn_readfirstlane(min(end, p.total_q)) - at.q0, 0);
       at.kv0 = at.nk = 0;
       if (at.local >= (at.nq * p.group + T::ROWS - 1) / T::ROWS) return false;
     } else if (!find_tile_spans(p, T::ROWS, at.local, lane, at)) {
@@ -458,6 +467,7 @@ struct Work {
       const int d = 16 * ks + 8 * half;
       qf[ks] = *reinterpret_cast<const bf16x8*>(q + min(d, p.head_dim - 8));
     }
+    if constexpr (SPANS) __builtin_amdgcn_sched_barrier(0);      // they leave here, not behind the first copies
 #pragma unroll
     for (int i = 0; i < H::DB; ++i)
 #pragma unroll
@@ -914,7 +924,9 @@ __global__ __launch_bounds__(NW * 64, H::DP == 64 ? 2 : 1) void attention_keys(c
   };
   int t = w.t0 + wave;
   w.start(t);
-  if (t < w.t1) {
+  // Two pieces: also past the last tile (of nothing), so that Q can be waited for without
+  // these copies: no branch between them.
+  if (SPANS || t < w.t1) {
     w.copy_k(k0s, NW);
     w.copy_v(v0s, NW);
   }

@@ -40,8 +40,7 @@ __global__ __launch_bounds__(256) void attention_join_spans(const SpanParams p) 
   if (!p.cu_q) b = 0;
   if (b < 0) return;
   int q0, nq, kv0, nk;
-  span_uniform(p.cu_q, b, p.total_q, q0, nq);
-  span_uniform(p.cu_k, b, p.total_k, kv0, nk);
+  spans_of(p, b, q0, nq, kv0, nk);
   const int token = query - q0;
   if (token < 0 || token >= nq) return;
   const int shares = p.shares(p.keys(nk)), all = shares + p.pre_splits;
