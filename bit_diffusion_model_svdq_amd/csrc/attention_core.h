@@ -111,9 +111,16 @@ struct SpanParams : Params {
   int prefix;            // shared keys; 0 with a window or sinks
   int reach;             // own keys that a tile sees at most (sinks and window), for the shares
   int pre_splits, pre_tiles, pre_blocks;   // shares of the cut-off prefix, tiles of all rows; the launch's first workgroups
-  Quotient by_heads, by_heads_q, by_group, by_tiles, by_pre_tiles;
+  // The launch's tiles from tail_tile on are cut into tail_splits shares (0: none are), its workgroups
+  // from tail_block on: what would be a last round of few tiles is spread over all CUs.
+  int tail_tile, tail_splits, tail_block;
+  Quotient by_heads, by_heads_q, by_group, by_tiles, by_pre_tiles, by_tail_tiles;
 
   __device__ int keys(int nk) const { return min(nk, reach) + (pre_splits > 0 ? 0 : prefix); }
+  // The first partial row of share s of tail tile t and a key head.
+  __device__ int64_t tail_slot(int s, int t, int hk, int rows) const {
+    return ((int64_t)(s * (tiles - tail_tile) + t) * heads_kv + hk) * rows;
+  }
   // The partial row of share s (a cut-off prefix's first) of a query's row: sequences that
   // fill little of their tiles take no more room for it.
   __device__ int64_t slot(int s, int hk, int query, int in_group) const {
@@ -328,6 +335,7 @@ struct Work {
   int shares;                // of the sequence's keys
   bool partial;              // two pieces: the results go to the workspace, as this share
   int share;
+  int tail;                  // number of its tile among the tail's, or -1
   int t0, t1;                // key tiles of this share
   bf16x8 qf[H::KS];
   f32x16 o[H::DB];
@@ -391,11 +399,19 @@ struct Work {
       pre = block < p.pre_blocks;
       if (!pre) block -= p.pre_blocks;
     }
+    const bool in_tail = MODE == kRows && p.tail_splits > 0 && block >= p.tail_block;
+    if (in_tail) block -= p.tail_block;
     const int rest = p.by_heads.of(block);
     hk = block - rest * p.heads_kv;
-    const int split = (pre ? p.by_pre_tiles : p.by_tiles).of(rest);
+    int split = (pre ? p.by_pre_tiles : p.by_tiles).of(rest);
     Place at;
     at.local = rest - split * (pre ? p.pre_tiles : p.tiles);
+    tail = -1;
+    if (in_tail) {
+      split = p.by_tail_tiles.of(rest);
+      tail = rest - split * (p.tiles - p.tail_tile);
+      at.local = p.tail_tile + tail;
+    }
     if (pre) {
       const int begin = p.cu_q[0], end = p.cu_q[p.batch];      // batch > 1: not NULL
       at.q0 = __builtin_amdgcn_readfirstlane(min(max(begin, 0), p.total_q));
@@ -412,6 +428,8 @@ struct Work {
     shares = 1;
     if (pre)
       shares = p.pre_splits;
+    else if (in_tail)
+      shares = p.tail_splits;
     else if (p.splits > 1)
       shares = p.shares(p.keys(nk));
     partial = shares > 1 || p.pre_splits > 0;
@@ -667,7 +685,8 @@ struct Work {
     if (part) {
       int64_t slot;
       if constexpr (SPANS)
-        slot = p.slot(share, hk, q0 + token, head - hk * p.group);
+        slot = MODE == kRows && tail >= 0 ? p.tail_slot(share, tail, hk, T::ROWS) + (row - row0)
+                                          : p.slot(share, hk, q0 + token, head - hk * p.group);
       else
         slot = (int64_t)blockIdx.x * T::ROWS + (row - row0);
       if (half == 0) p.part_lse[slot] = lse2;

@@ -6,46 +6,29 @@
 namespace svdq {
 namespace {
 
-// Joins the shares of a row as attention_join does: a wave per query and head, whose partial
-// rows lie at SpanParams::slot.  Their weights and the first sixteen rows are loaded before it is known which
-// of them the sequence has: 64 tokens behind a prefix of 8192 7.4 -> 6.3 us, 16 with
-// windows of 1024 keys 7.3 -> 4.1.
-__global__ __launch_bounds__(256) void attention_join_spans(const SpanParams p) {
+// Joins the shares of a row as attention_join does: a wave per row, lane s holding share s's
+// weight.  The weights and the first sixteen rows of the `most` shares it can have are loaded before
+// find() says how many it has, and whose row it is (false: nobody's, or written by its one share): 64
+// tokens behind a prefix of 8192 7.4 -> 6.3 us, 16 with windows of 1024 keys 7.3 -> 4.1.
+struct JoinRow {
+  int shares, query, token, nq, nk;
+};
+template <class Slot, class Find>
+__device__ inline void join_row(const SpanParams& p, int lane, int most, int head, Slot slot, Find find) {
   constexpr int kAhead = 16;
-  const int lane = threadIdx.x & 63;
-  const int id = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int query = p.by_heads_q.of(id), head = id - query * p.heads_q;
-  if (query >= p.total_q) return;
-  const int hk = p.by_group.of(head);
-  const int most = p.pre_splits + p.splits;
   const int d = 2 * lane;
   const bool on = d < p.head_dim;
   float2 v[kAhead];
   auto load = [&](int s0) {
 #pragma unroll
     for (int u = 0; u < kAhead; ++u)
-      if (s0 + u < most)
-        v[u] = *reinterpret_cast<const float2*>(p.part + p.slot(s0 + u, hk, query, head - hk * p.group) * p.head_dim +
-                                                (on ? d : 0));
+      if (s0 + u < most) v[u] = *reinterpret_cast<const float2*>(p.part + slot(s0 + u) * p.head_dim + (on ? d : 0));
   };
-  float e = lane < most ? p.part_lse[p.slot(lane, hk, query, head - hk * p.group)] : -INFINITY;
+  float e = lane < most ? p.part_lse[slot(lane)] : -INFINITY;
   load(0);
-  // the last sequence that begins at or before the query, 64 at a time
-  int b = -1;
-  for (int base = 0; base < p.batch && p.cu_q; base += 64) {
-    const uint64_t m = __ballot(base + lane < p.batch && p.cu_q[min(base + lane, p.batch - 1)] <= query);
-    b += __builtin_popcountll(m);
-    if (m != ~uint64_t(0)) break;
-  }
-  if (!p.cu_q) b = 0;
-  if (b < 0) return;
-  int q0, nq, kv0, nk;
-  spans_of(p, b, q0, nq, kv0, nk);
-  const int token = query - q0;
-  if (token < 0 || token >= nq) return;
-  const int shares = p.shares(p.keys(nk)), all = shares + p.pre_splits;
-  if (all == 1) return;                                  // written by its one share
-  if (lane >= all) e = -INFINITY;
+  JoinRow r;
+  if (!find(r)) return;
+  if (lane >= r.shares) e = -INFINITY;
   float top = e;
 #pragma unroll
   for (int s = 32; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor(top, s));
@@ -54,11 +37,11 @@ __global__ __launch_bounds__(256) void attention_join_spans(const SpanParams p) 
 #pragma unroll
   for (int s = 32; s > 0; s >>= 1) sum += __shfl_xor(sum, s);
   float a0 = 0.f, a1 = 0.f;
-  for (int s0 = 0; s0 < all; s0 += kAhead) {
+  for (int s0 = 0; s0 < r.shares; s0 += kAhead) {
     if (s0 > 0) load(s0);
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      if (s0 + u >= all) break;
+      if (s0 + u >= r.shares) break;
       const float w = __shfl(weight, s0 + u);
       if (w != 0.f) {                                    // a share without weight has written nothing
         a0 = __builtin_fmaf(w, v[u].x, a0);
@@ -67,17 +50,65 @@ __global__ __launch_bounds__(256) void attention_join_spans(const SpanParams p) 
     }
   }
   // as in finish(): no weight at all is NaN for a query that sees keys
-  const bool seen = p.sees(token, nq, nk);
+  const bool seen = p.sees(r.token, r.nq, r.nk);
   const bool none = sum == 0.f;
   const float inv = !none ? 1.f / sum : seen ? NAN : 0.f;
   if (on) {
     const uint16_t x = __builtin_bit_cast(uint16_t, (__bf16)(a0 * inv));
     const uint16_t y = __builtin_bit_cast(uint16_t, (__bf16)(a1 * inv));
-    *reinterpret_cast<uint32_t*>(p.O + (int64_t)query * p.ldo + (int64_t)head * p.head_dim + d) = x | ((uint32_t)y << 16);
+    *reinterpret_cast<uint32_t*>(p.O + (int64_t)r.query * p.ldo + (int64_t)head * p.head_dim + d) = x | ((uint32_t)y << 16);
   }
   if (p.lse && lane == 0)
-    p.lse[(int64_t)head * p.total_q + query] =
+    p.lse[(int64_t)head * p.total_q + r.query] =
         !none ? (top + __builtin_amdgcn_logf(sum)) * kLn2 : seen ? NAN : -INFINITY;
+}
+
+// Every query and head, with partial rows at SpanParams::slot.
+__global__ __launch_bounds__(256) void attention_join_spans(const SpanParams p) {
+  const int lane = threadIdx.x & 63;
+  const int id = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int query = p.by_heads_q.of(id), head = id - query * p.heads_q;
+  if (query >= p.total_q) return;
+  const int hk = p.by_group.of(head);
+  auto slot = [&](int s) { return p.slot(s, hk, query, head - hk * p.group); };
+  join_row(p, lane, p.pre_splits + p.splits, head, slot, [&](JoinRow& r) {
+    // the last sequence that begins at or before the query, 64 at a time
+    int b = p.cu_q ? -1 : 0;
+    for (int base = 0; base < p.batch && p.cu_q; base += 64) {
+      const uint64_t m = __ballot(base + lane < p.batch && p.cu_q[min(base + lane, p.batch - 1)] <= query);
+      b += __builtin_popcountll(m);
+      if (m != ~uint64_t(0)) break;
+    }
+    if (b < 0) return false;
+    int q0, kv0;
+    spans_of(p, b, q0, r.nq, kv0, r.nk);
+    r.query = query;
+    r.token = query - q0;
+    r.shares = p.shares(p.keys(r.nk)) + p.pre_splits;
+    return r.token >= 0 && r.token < r.nq && r.shares > 1;
+  });
+}
+
+// The rows of the tail's tiles, with partial rows at SpanParams::tail_slot.
+__global__ __launch_bounds__(256) void attention_join_tail(const SpanParams p) {
+  constexpr int kRowsPerTile = 4 * kWaveRows;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int rest = p.by_heads.of(blockIdx.x), hk = blockIdx.x - rest * p.heads_kv;
+  const int t = rest / (kRowsPerTile / 4), in_tile = rest % (kRowsPerTile / 4) * 4 + wave;
+  Place at;
+  if (!find_tile_spans(p, kRowsPerTile, p.tail_tile + t, lane, at)) return;
+  const int nrows = at.nq * p.group;
+  int local = at.local;
+  if (p.causal) local = (nrows + kRowsPerTile - 1) / kRowsPerTile - 1 - local;
+  const int row = local * kRowsPerTile + in_tile;
+  if (row >= nrows) return;
+  const int token = p.by_group.of(row), head = hk * p.group + row - token * p.group;
+  auto slot = [&](int s) { return p.tail_slot(s, t, hk, kRowsPerTile) + in_tile; };
+  join_row(p, lane, p.tail_splits, head, slot, [&](JoinRow& r) {
+    r = {p.tail_splits, at.q0 + token, token, at.nq, at.nk};
+    return true;
+  });
 }
 
 // Partial rows of a cut-off prefix that a call may ask its caller to hold: 8192 new tokens x 32 x 128.
@@ -134,6 +165,42 @@ void offer_cut(const SpanArgs& a, int64_t rows, SpanPlan& sp) {
   sp.own.tiles = tiles;
 }
 
+// attention_rows with four waves and shares for the tiles of a last, partly filled round, if that
+// is less than the plan at hand.  A CU takes one tile of rows in 0.58 of the time of two at once, so
+// with k whole rounds of one per CU and a part of the next the launch lasts nearly as long as
+// with k + 1; cut into so many shares that they fill it, the rest lasts that much less.  Counted
+// for as much of the tiles' keys as is alike in all of them: where they differ (causal, the
+// ends of windows) the tiles fill the gaps themselves.  Measured, before and with shares: prefix of 3000
+// and 1408 tokens x 24 x 128 135 / 112 us, 1792 147 / 128, 2816 294 / 212; prefix of 800 and 2816 tokens 188 / 143;
+// ragged continuations of 4001 keys, 1076 tokens x 32 / 8 x 128, 119 / 106.  Windows of 1500 to both sides of
+// 2816 and 3328 tokens, whose tiles differ, would gain 106 / 100 and 120 / 121: not taken.
+void offer_tail(const SpanArgs& a, int64_t rows, SpanPlan& sp) {
+  const int64_t cus = device_cu_count();
+  constexpr int kHeight = 4 * kWaveRows;
+  const int64_t tiles = std::min<int64_t>(rows / kHeight + a.batch, rows);
+  const double units = std::min(std::ceil((double)rows / a.batch / kHeight) * a.batch, (double)tiles) * a.heads_kv;
+  const int64_t whole = (int64_t)(units / cus), first = whole * cus / a.heads_kv, tail = tiles - first;
+  const double rest = (units - first * a.heads_kv) / cus;
+  if (whole < 1 || whole > 6 || rest < 0.02 || rest > 0.5 || tail < 1) return;
+  const int shares = (int)std::min(8.0, 1 / rest);
+  const double window = window_of(a), mean_own = (double)a.total_k / a.batch, mean_q = (double)a.total_q / a.batch;
+  double own = std::min(mean_own, window + std::min(mean_q, (double)kHeight * a.heads_kv / a.heads_q));
+  if (a.causal && mean_own <= window) own *= 1 - 0.4 * std::min(1.0, mean_q / std::max(mean_own, 1.0));
+  const bool alike = window == INFINITY ? !a.causal : mean_own > 2 * window;
+  const double keys = own + a.prefix, cost = 2 * cost_of(a.head_dim).rows4_each / 32;      // us of a key for two workgroups
+  const double gain = (whole % 2 ? 0.42 : 0.58) * (1 - 1.0 / shares) * cost * (alike ? keys : a.prefix);
+  const int64_t slots = tail * a.heads_kv * shares * kHeight;
+  const double us = cost * keys * (whole / 2 + (whole % 2 ? 1.0 : 0.58)) - gain + 6.0 + 2e-6 * slots * a.head_dim;
+  if (us >= sp.own.us || gain < 6.0 + 2e-6 * slots * a.head_dim || slots * (a.head_dim + 1) * 4 > int64_t(64) << 20) return;
+  sp.own = Plan();
+  sp.own.rows = kHeight;
+  sp.own.tiles = tiles;
+  sp.own.chunk = 128;
+  sp.own.us = us;
+  sp.tail_tile = (int)first;
+  sp.tail_splits = shares;
+}
+
 // A prefix is cut off where that is less work by the same estimate as in plan_of: new
 // tokens of several sequences, each of which would otherwise read it for itself, with most
 // of the MFMA's 32 columns idle.
@@ -143,10 +210,20 @@ SpanPlan plan_spans(const SpanArgs& a) {
   const int64_t rows = (int64_t)a.total_q * group;
   sp.own = plan_of(a.total_q, a.total_k, a.batch, a.heads_q, a.heads_kv, a.head_dim, a.causal != 0, window_of(a),
                    a.prefix);
-  if (a.prefix > 0 && a.batch > 1 && rows <= (int64_t)a.batch * kTokenRows) offer_cut(a, rows, sp);
+  if (rows > (int64_t)a.batch * kTokenRows)
+    offer_tail(a, rows, sp);
+  else if (a.prefix > 0 && a.batch > 1)
+    offer_cut(a, rows, sp);
   sp.blocks = (sp.own.tiles * sp.own.splits + (int64_t)sp.pre_tiles * sp.pre_splits) * a.heads_kv;
   sp.most_blocks = sp.blocks;
-  if (sp.own.splits > 1 || sp.pre_splits > 0) {
+  if (sp.tail_splits > 0) {
+    const int64_t tail = sp.own.tiles - sp.tail_tile;
+    sp.blocks += tail * (sp.tail_splits - 1) * a.heads_kv;
+    const size_t slots = (size_t)tail * a.heads_kv * sp.tail_splits * sp.own.rows;
+    sp.part = (slots * a.head_dim * 4 + 255) & ~size_t(255);
+    sp.bytes = sp.part + ((slots * 4 + 255) & ~size_t(255));
+    sp.most_blocks = std::max(sp.blocks, tail * a.heads_kv * (sp.own.rows / 4));
+  } else if (sp.own.splits > 1 || sp.pre_splits > 0) {
     const size_t slots = (size_t)rows * a.heads_kv * (sp.pre_splits + sp.own.splits);
     sp.part = (slots * a.head_dim * 4 + 255) & ~size_t(255);
     sp.bytes = sp.part + ((slots * 4 + 255) & ~size_t(255));
@@ -173,6 +250,11 @@ hipError_t launch(const SpanPlan& sp, const SpanParams& p, hipStream_t stream) {
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || sp.bytes == 0) return e;
+  if (sp.tail_splits > 0) {
+    const int64_t blocks = (pl.tiles - sp.tail_tile) * p.heads_kv * (pl.rows / 4);
+    hipLaunchKernelGGL(attention_join_tail, dim3((unsigned)blocks), dim3(256), 0, stream, p);
+    return hipGetLastError();
+  }
   hipLaunchKernelGGL(attention_join_spans, dim3((unsigned)join_blocks(p.total_q, p.heads_q)), dim3(256), 0, stream, p);
   return hipGetLastError();
 }
@@ -202,6 +284,10 @@ hipError_t launch_attention_spans(const SpanArgs& a, const SpanPlan& sp, hipStre
   p.pre_splits = sp.pre_splits;
   p.pre_tiles = sp.pre_tiles;
   p.pre_blocks = sp.pre_splits * sp.pre_tiles * a.heads_kv;
+  p.tail_tile = sp.tail_tile;
+  p.tail_splits = sp.tail_splits;
+  p.tail_block = sp.tail_tile * a.heads_kv;
+  p.by_tail_tiles = Quotient((int)std::max<int64_t>(sp.own.tiles - sp.tail_tile, 1));
   p.by_heads = Quotient(a.heads_kv);
   p.by_heads_q = Quotient(a.heads_q);
   p.by_group = Quotient(p.group);

@@ -148,6 +148,13 @@ def test_a_window_cut_into_shares():
         c.call().check()
 
 
+def test_the_last_tiles_of_a_long_window_are_cut_into_shares():
+    c = Case([6144], [6144], 6, 6, 96, True, (3000, 0, 4))
+    if CUS == 256:
+        assert c.bytes() > 0
+    c.call().check()
+
+
 @pytest.mark.parametrize("nq", [1, 3])
 @pytest.mark.parametrize("d,hq,hkv", [(128, 32, 8), (64, 4, 4)])
 def test_keys_that_a_cache_has_given_up_may_hold_anything(nq, d, hq, hkv):
@@ -229,9 +236,20 @@ FORMS = {
     "prefix keys": lambda **k: Case([90, 200, 33], [90, 200, 33], 4, 4, 64, True, prefix=70, **k),
     "prefix rows": lambda **k: Case([127, 0, 130, 5, 129], [127, 0, 130, 5, 129], 96, 96, 96, True, prefix=150, **k),
     "prefix rows8": lambda **k: Case([254, 241], [254, 241], 96, 96, 128, False, prefix=99, **k),
+    "prefix tail": lambda **k: Case([300, 1, 460], [300, 1, 460], 48, 48, 128, True, prefix=4000, **k),
+    "prefix tail 64": lambda **k: Case([260, 0, 700, 300], [9, 5, 700, 0], 28, 28, 64, False, prefix=5000, **k),
     "prefix shares": lambda **k: Case([100, 90], [100, 90], 4, 4, 128, True, prefix=5000, **k),
 }
 forms = pytest.mark.parametrize("form", FORMS, ids=lambda s: s.replace(" ", "_"))
+
+
+@forms
+def test_forms_that_join_shares(form):
+    """By the workspace that they ask for, on the card that they are planned for."""
+    if CUS != 256:
+        pytest.skip("planned for 256 compute units")
+    joined = any(w in form for w in ("shares", "tail")) or form in ("window tokens", "prefix tokens")
+    assert (FORMS[form]().bytes() > 0) == joined
 
 
 @forms
