@@ -201,6 +201,36 @@ void offer_tail(const SpanArgs& a, int64_t rows, SpanPlan& sp) {
   sp.tail_splits = shares;
 }
 
+// attention_keys with four waves for heads of more than 64 channels where a CU has one workgroup at
+// most, so that nothing runs beside it anyway, and for new tokens that instead of shares and a
+// second launch as long as the longest sequence, taken to be twice the average, has five turns
+// of their four tiles.  It is no gain for two turns of two waves.  Measured, two / four waves: 8 single
+// tokens x 16 / 4 x 128 with 64 keys, 128, 256 6.7 / 7.7 us, 8.4 / 8.0, 10.9 / 9.5, and with one of 544 among
+// 1 to 160 18.8 / 13.3; 7 of up to 848 keys x 8 x 72 22.9 / 15.7; prompts of 77, 160, 320 tokens x 8 / 4 x 128
+// 6.9 / 6.9, 9.0 / 9.2, 11.7 / 10.8; in shares / four waves: 384 keys 14.0 / 10.8, with windows of 516 13.9 / 13.6,
+// 8 x 16 / 4 x 96 with up to 1280 keys, on average 500, 14.6 / 17.8.  Eight waves for 64 channels: 128 keys 5.4 / 6.5,
+// 512 7.7 / 8.5, 1024 11.2 / 10.2: not taken.
+constexpr int kWideWaves = 4;
+void offer_wide(const SpanArgs& a, int64_t rows, SpanPlan& sp) {
+  const int64_t cus = device_cu_count();
+  const int group = a.heads_q / a.heads_kv;
+  const double mean_own = (double)a.total_k / a.batch, mean_q = (double)a.total_q / a.batch;
+  const double longest = std::min(mean_own * (a.batch > 1 ? 2 : 1), window_of(a) + std::min(mean_q, (double)kWaveRows / group)) + a.prefix;
+  const double key_tiles = std::ceil(longest / 32);
+  const int64_t tiles = std::min<int64_t>(rows / kWaveRows + a.batch, rows);
+  const bool shares = sp.own.splits > 1 || sp.pre_splits > 0;
+  if (shares && rows <= (int64_t)a.batch * kTokenRows && tiles * a.heads_kv <= cus && key_tiles <= 5 * kWideWaves) {
+    sp = SpanPlan();
+    sp.own.keys = true;
+    sp.own.parts = 2;
+    sp.own.rows = kWaveRows;
+    sp.own.tiles = tiles;
+    sp.own.chunk = 128;
+  }
+  const int64_t blocks = (sp.own.tiles * sp.own.splits + (int64_t)sp.pre_tiles * sp.pre_splits) * a.heads_kv;
+  sp.wide = sp.own.keys && blocks <= cus && (sp.own.splits > 1 || sp.pre_splits > 0 || key_tiles > 2 * key_waves(128));
+}
+
 // A prefix is cut off where that is less work by the same estimate as in plan_of: new
 // tokens of several sequences, each of which would otherwise read it for itself, with most
 // of the MFMA's 32 columns idle.
@@ -214,6 +244,7 @@ SpanPlan plan_spans(const SpanArgs& a) {
     offer_tail(a, rows, sp);
   else if (a.prefix > 0 && a.batch > 1)
     offer_cut(a, rows, sp);
+  if (a.head_dim > 64) offer_wide(a, rows, sp);
   sp.blocks = (sp.own.tiles * sp.own.splits + (int64_t)sp.pre_tiles * sp.pre_splits) * a.heads_kv;
   sp.most_blocks = sp.blocks;
   if (sp.tail_splits > 0) {
@@ -237,11 +268,17 @@ hipError_t launch(const SpanPlan& sp, const SpanParams& p, hipStream_t stream) {
   const Plan& pl = sp.own;
   const dim3 grid((unsigned)sp.blocks);
   if (pl.keys) {
-    constexpr int kWaves = key_waves(H::DP);
-    if (pl.parts == 2)
-      hipLaunchKernelGGL((attention_keys<H, kWaves, 2, true>), grid, dim3(kWaves * 64), 0, stream, p);
+    auto go = [&](auto waves) {
+      constexpr int kWaves = decltype(waves)::value;
+      if (pl.parts == 2)
+        hipLaunchKernelGGL((attention_keys<H, kWaves, 2, true>), grid, dim3(kWaves * 64), 0, stream, p);
+      else
+        hipLaunchKernelGGL((attention_keys<H, kWaves, 1, true>), grid, dim3(kWaves * 64), 0, stream, p);
+    };
+    if (sp.wide)
+      go(std::integral_constant<int, kWideWaves>());
     else
-      hipLaunchKernelGGL((attention_keys<H, kWaves, 1, true>), grid, dim3(kWaves * 64), 0, stream, p);
+      go(std::integral_constant<int, key_waves(H::DP)>());
   } else if (pl.waves == 8) {
     if constexpr (H::DP == 128)
       hipLaunchKernelGGL((attention_rows<H, 8, true>), grid, dim3(512), 0, stream, p);

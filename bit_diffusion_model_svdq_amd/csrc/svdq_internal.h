@@ -205,6 +205,7 @@ struct SpanArgs : AttentionArgs {
 struct SpanPlan {
   AttentionPlan own;      // the whole work, or with a cut-off prefix that against the own keys
   int pre_splits = 0, pre_tiles = 0;
+  bool wide = false;      // attention_keys with four waves where it has two
   int tail_tile = 0, tail_splits = 0;      // shares of the launch's last tiles, 0: whole
   int64_t blocks = 0;     // workgroups of the launch
   int64_t most_blocks = 0;     // and of the largest of its launches

@@ -232,6 +232,8 @@ FORMS = {
     "window rows": lambda **k: Case([127, 0, 130, 5, 129], [127, 0, 130, 5, 129], 96, 96, 64, True, (40, 0, 2), **k),
     "window rows8": lambda **k: Case([254, 241], [254, 241], 96, 96, 128, False, (60, 70, 3), **k),
     "window shares": lambda **k: Case([200], [4000], 2, 2, 64, False, (3000, 700, 40), **k),
+    "window wide": lambda **k: Case([1, 2, 1], [390, 0, 700], 8, 2, 128, True, (200, 0, 9), **k),
+    "prefix wide": lambda **k: Case([1, 2, 1, 3], [50, 700, 0, 3], 6, 3, 96, True, prefix=150, **k),
     "prefix tokens": lambda **k: Case([1, 2, 1, 1], [50, 700, 0, 3], 8, 2, 128, True, prefix=3000, **k),
     "prefix keys": lambda **k: Case([90, 200, 33], [90, 200, 33], 4, 4, 64, True, prefix=70, **k),
     "prefix rows": lambda **k: Case([127, 0, 130, 5, 129], [127, 0, 130, 5, 129], 96, 96, 96, True, prefix=150, **k),
@@ -337,7 +339,8 @@ def test_bad_queries_reach_their_rows_alone(form):
 
 @forms
 def test_scores_out_of_range(form):
-    """A query that sees keys, all of whose scores are -inf or overflow, gets NaN; one +inf among them too."""
+    """A query that sees keys, all of whose scores are -inf or overflow, gets NaN; one +inf among them too; one
+    that sees none is not touched by any of it."""
     c = FORMS[form](scale=1.0)
     c.K.fill_(0), c.Q.fill_(0)
     if c.PK is not None:
@@ -349,8 +352,12 @@ def test_scores_out_of_range(form):
     c.Q[row, 0, 0] = -1e38
     c.call()
     torch.cuda.synchronize()
-    r = slice(int(c.cu_q[0]), int(c.cu_q[-1]))
-    assert torch.isnan(c.O[r]).all() and torch.isnan(c.lse[:, r]).all()
+    some = [B.sees(int(nq), int(nk), c.causal, *c.window).any(1) | (c.PK is not None)
+            for nq, nk in zip(np.diff(c.cu_q), np.diff(c.cu_k))]
+    some = torch.from_numpy(np.concatenate(some)).to(DEV)
+    O, lse = c.O[int(c.cu_q[0]):int(c.cu_q[-1])], c.lse[:, int(c.cu_q[0]):int(c.cu_q[-1])]
+    assert torch.isnan(O[some]).all() and torch.isnan(lse[:, some]).all()
+    assert (O[~some] == 0).all() and (lse[:, ~some] == -float("inf")).all()      # a query that sees no key
 
 
 @forms
