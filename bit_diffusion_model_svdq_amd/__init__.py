@@ -770,11 +770,18 @@ def svdq_attention_forward(Q, K, V, cu_q, cu_k, scale, causal, O, lse=None, work
     return O
 
 
+def _key_limit(n):
+    """A number of keys as the library takes it, in 32 bits, of which ctypes would keep the low ones:
+    no sequence has more keys than they hold, and below -1 all are refused alike."""
+    return n if -2 <= n < 2**31 else 2**31 - 1 if n > 0 else -2
+
+
 def svdq_attention_window_workspace_bytes(total_q: int, total_k: int, batch: int, heads_q: int, heads_kv: int,
                                           head_dim: int, causal: bool, window_left: int, window_right: int,
                                           sinks: int) -> int:
     return int(_lib.svdq_attention_window_workspace_bytes(total_q, total_k, batch, heads_q, heads_kv, head_dim,
-                                                          int(causal), window_left, window_right, sinks))
+                                                          int(causal), _key_limit(window_left),
+                                                          _key_limit(window_right), _key_limit(sinks)))
 
 
 def svdq_attention_window_forward(Q, K, V, cu_q, cu_k, scale, causal, window_left, window_right, sinks, O, lse=None,
@@ -784,9 +791,11 @@ def svdq_attention_window_forward(Q, K, V, cu_q, cu_k, scale, causal, window_lef
     them up to p."""
     index, ldq, ldk, ldv, ldo, batch, total_q, total_k, heads_q, heads_kv, d = _attention_operands(
         Q, K, V, cu_q, cu_k, O, lse, workspace)
+    if not (-2 < window_left < 2**31 and -2 < window_right < 2**31 and -1 < sinks < 2**31):
+        window_left, window_right, sinks = _key_limit(window_left), _key_limit(window_right), _key_limit(sinks)
     _launch(index, stream, _lib.svdq_attention_window_forward, Q.data_ptr(), ldq, K.data_ptr(), ldk, V.data_ptr(), ldv,
-            _ptr(cu_q), _ptr(cu_k), batch, total_q, total_k, heads_q, heads_kv, d, scale, int(causal), window_left,
-            window_right, sinks, O.data_ptr(), ldo, _ptr(lse), _ptr(workspace), _bytes(workspace))
+            _ptr(cu_q), _ptr(cu_k), batch, total_q, total_k, heads_q, heads_kv, d, scale, int(causal),
+            window_left, window_right, sinks, O.data_ptr(), ldo, _ptr(lse), _ptr(workspace), _bytes(workspace))
     return O
 
 
