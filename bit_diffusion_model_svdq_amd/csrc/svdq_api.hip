@@ -270,10 +270,18 @@ svdq_status linear_forward_mx(const uint16_t* X, int M, int K, int N, int r, con
 constexpr int64_t kMaxBlocks = (int64_t(1) << 23) - 1;
 // Heads that svdq_qk_norm_rope_forward counts in 32 bits, with their steps.
 constexpr int kMaxHeads = 1 << 20;
+// Sequences whose offsets a kernel looks up 64 at a time, in 32 bits.
+constexpr int kMaxBatch = INT32_MAX - 512;
+
+svdq_status check_batch(int batch) {
+  if (batch < 1 || batch > kMaxBatch)
+    return fail(SVDQ_ERR_INVALID_ARG, "batch must be 1 to %d (got %d)", kMaxBatch, batch);
+  return SVDQ_OK;
+}
 
 svdq_status check_attention_shape(int batch, int64_t total_q, int64_t total_k, int heads_q, int heads_kv,
                                   int head_dim, bool count_blocks = true) {
-  if (batch < 1) return fail(SVDQ_ERR_INVALID_ARG, "batch must be >= 1 (got %d)", batch);
+  SVDQ_TRY(check_batch(batch));
   if (total_q < 0 || total_k < 0)
     return fail(SVDQ_ERR_INVALID_ARG, "negative total_q=%lld or total_k=%lld", (long long)total_q,
                 (long long)total_k);
@@ -741,7 +749,7 @@ svdq_status svdq_qk_norm_rope_forward(const uint16_t* Q, int64_t ldq, const uint
     if (head_dim < 8 || head_dim % 8)
       return fail(SVDQ_ERR_INVALID_ARG, "head_dim must be a positive multiple of 8 (got %d)", head_dim);
     if (head_dim > kMaxRopeHead) return fail(SVDQ_ERR_UNSUPPORTED, "head_dim %d is above %d", head_dim, kMaxRopeHead);
-    if (batch < 1) return fail(SVDQ_ERR_INVALID_ARG, "batch must be >= 1 (got %d)", batch);
+    SVDQ_TRY(check_batch(batch));
     if (batch > 1 && !cu) return fail(SVDQ_ERR_INVALID_ARG, "cu must not be NULL for batch=%d", batch);
     SVDQ_TRY(check_norm(norm, "norm"));
     if (!(eps >= 0.f) || !isfinite(eps))

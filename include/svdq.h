@@ -377,7 +377,8 @@ svdq_status svdq_quantize_activations_mxfp4(const uint16_t* X, int M, int K, con
  * their offsets, ascending; sequence b is rows [cu[b], cu[b + 1]).  Rows before
  * cu[0] and from cu[batch] on belong to no sequence: they are not read, and
  * the outputs' rows there stay as they were.  A sequence may be empty.  cu
- * may be NULL for batch = 1: one sequence of all rows.  The offsets are read
+ * may be NULL for batch = 1: one sequence of all rows.  Attention and the norm
+ * and rotation of queries and keys take at most 2^31 - 513 sequences.  The offsets are read
  * by the kernels, never by the host; whatever they hold, no kernel accesses
  * anything outside the tensors' rows (offsets that do not ascend give
  * undefined results). */
