@@ -115,7 +115,7 @@ __device__ inline int sequence_of(const int32_t* cu, int batch, int64_t row) {
   if (row < cu[0] || row >= cu[batch]) return -1;
   int lo = 0, hi = batch;
   while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
+    const int mid = lo + ((hi - lo) >> 1);      // lo + hi may pass 31 bits
     if (cu[mid] <= row)
       lo = mid;
     else
