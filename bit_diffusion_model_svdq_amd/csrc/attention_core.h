@@ -734,7 +734,8 @@ struct Work {
 // and laid out by hand in pieces of two or three MFMAs with a few softmax
 // elements after each (VALU work issues beside a running MFMA of its own
 // wave): the scores of tile t + 1 beside the weights of tile t, then P V of tile
-// t beside the rest of them.  Tiles of 32 keys: with 64 the scores of two tiles
+// t beside the rest of them.  The compiler keeps the exponentials there and sinks the
+// sum's 17 additions behind the tile's last MFMA.  Tiles of 32 keys: with 64 the scores of two tiles
 // spill.  One path for every tile, with the mask as the one thing that branches:
 // variants of the tile make the compiler spill or merge their weights into one
 // block away from the MFMAs.
@@ -749,6 +750,13 @@ struct Work {
 // with 8 waves and 2.97 ms with 4, though the 4 waves' form needs 11 % fewer
 // cycles (5.1 M against 5.7 M): it moves twice the bytes from L2 and the clock
 // drops to 1.71 GHz (1.95).  MFMAs run in 62 % (55 %) of the cycles.
+//
+// With SPANS it is the loop itself that bounds them: between a turn's barrier and its first
+// MFMA stand about 50 scalar instructions, five branches and eight register moves (the
+// piece, its stride and the lanes' offsets, for K and for V), where the plain form has 11 to 16
+// and one branch, and another chain of branches behind the MFMAs (whole()).  MFMAs run in
+// 47 % of the cycles of 16384 tokens x 24 x 128 with windows of 2048 to both sides
+// (824 to 838 us), in 41 % behind a prefix of 4608 keys (4 x 1024 tokens, 303 us).
 template <class H, int NW, bool SPANS>
 __global__ __launch_bounds__(NW * 64, 2) void attention_rows(const typename ParamsOf<SPANS>::type p) {
   using T = Tile<H, kRows, NW>;

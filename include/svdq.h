@@ -452,9 +452,10 @@ svdq_status svdq_attention_window_forward(const uint16_t* Q, int64_t ldq, const 
  * apart, as ldk and ldv), then the keys of its own sequence (causal: those up to its
  * own, as there).  One softmax over both; the prefix is stored once, and calls of at most 64
  * rows per sequence also read and compute it once for all sequences where that is less work.
- * Then the softmax's weights enter the product with V rounded to bf16 where there are many
- * rows, with 15 bits where there are few.  Everything else is svdq_attention_forward's; either
- * of the two pieces may be empty, also for some of the sequences.  prefix_len + total_k: at
+ * Then the softmax's weights enter the product with V rounded to bf16 from 128 rows (total_q
+ * times G) on, or where the sequences (at most the rows) times heads_kv are twice the
+ * compute units or more, and with 15 bits below.  Everything else is svdq_attention_forward's;
+ * either of the two pieces may be empty, also for some of the sequences.  prefix_len + total_k: at
  * most 2^31 - 513.  The workspace of new tokens grows with them (partial rows of float32), to
  * at most 257 MiB. */
 size_t svdq_attention_prefix_workspace_bytes(int64_t total_q, int64_t prefix_len, int64_t total_k, int batch,
