@@ -111,7 +111,8 @@ __global__ __launch_bounds__(256) void attention_join_tail(const SpanParams p) {
   });
 }
 
-// Partial rows of a cut-off prefix that a call may ask its caller to hold: 8192 new tokens x 32 x 128.
+// Partial rows of a cut-off prefix that a call may ask its caller to hold: those of 8128 new tokens x 32 x 128,
+// with one share of the prefix and one of the own keys.
 constexpr int64_t kMaxSplitBytes = int64_t(256) << 20;
 
 // Workgroups of the join.
